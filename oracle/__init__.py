@@ -5,3 +5,4 @@ from .rnnt_oracle import (STATUS_BOUNDS, STATUS_LABEL, STATUS_LENGTH, OracleResu
                           validate_bounds, viterbi_lattice)
 from .tdt_oracle import (STATUS_DURATIONS, TdtResult, tdt_alpha, tdt_beta, tdt_edge_posteriors,  # noqa: F401
                          tdt_fwd_bwd, tdt_log_p_from_alpha, tdt_loss_only, validate_durations)
+from . import ops_oracle  # noqa: F401

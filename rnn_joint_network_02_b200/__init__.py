@@ -7,3 +7,5 @@ for B200 (sm_100a), behind the C ABI declared in include/frnnt.h.
 
 from . import frnnt  # noqa: F401
 from .frnnt import fwd_bwd, workspace_size  # noqa: F401
+from .frnnt import (dropout, recurrence, recurrence_bwd, recurrence_step, token_logprobs,  # noqa: F401
+                    token_logprobs_bwd)

@@ -2,6 +2,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <mutex>
 #include <vector>
 
 #include "frnnt_internal.h"
@@ -21,8 +22,11 @@ struct Pending {
   cudaEvent_t start, stop;
 };
 
+// Stages and events are shared by all host threads (calls may come from
+// several at once); launches are counted per thread, so a stage counts its own.
+std::mutex g_mu;
 bool g_timing = false;
-long long g_launches = 0;
+thread_local long long t_launches = 0;
 std::vector<Stage> g_stages;
 std::vector<Pending> g_pending;
 std::vector<cudaEvent_t> g_free_events;
@@ -50,7 +54,7 @@ cudaEvent_t take_event() {
 
 }  // namespace
 
-void note_launch(int n) { g_launches += n; }
+void note_launch(int n) { t_launches += n; }
 
 // ---------------------------------------------------------------- launch chaining (per host thread)
 namespace {
@@ -85,7 +89,8 @@ void chain_note(cudaStream_t st) {
   if (t_chain.active && st == t_chain.st) t_chain.armed = true;
 }
 
-StageScope::StageScope(const char* name, cudaStream_t st) : st_(st), launches0_(g_launches) {
+StageScope::StageScope(const char* name, cudaStream_t st) : st_(st), launches0_(t_launches) {
+  std::lock_guard<std::mutex> guard(g_mu);
   stage_ = stage_index(name);
   if (g_timing) {
     start_ = take_event();
@@ -95,8 +100,9 @@ StageScope::StageScope(const char* name, cudaStream_t st) : st_(st), launches0_(
 }
 
 StageScope::~StageScope() {
+  std::lock_guard<std::mutex> guard(g_mu);
   Stage& s = g_stages[stage_];
-  s.launches += (int)(g_launches - launches0_);
+  s.launches += (int)(t_launches - launches0_);
   s.calls += 1;
   if (g_timing && start_) {
     cudaEvent_t stop = take_event();
@@ -120,6 +126,7 @@ extern "C" FRNNT_API int frnnt_profile(int enable) {
 }
 
 extern "C" FRNNT_API int frnnt_profile_read(frnnt_stage_stat* out, int capacity, int* count) {
+  std::lock_guard<std::mutex> guard(g_mu);
   int rc = FRNNT_OK;
   for (const Pending& p : g_pending) {
     float ms = 0.f;

@@ -21,11 +21,14 @@ F32, BF16 = 0, 1
 PATH_AUTO, PATH_SIMT = 0, 1
 
 OK = 0
-STATUS_LENGTH, STATUS_LABEL, STATUS_TIMEOUT, STATUS_BOUNDS = 1, 2, 4, 8
+STATUS_LENGTH, STATUS_LABEL, STATUS_TIMEOUT, STATUS_BOUNDS, STATUS_INDEX = 1, 2, 4, 8, 16
 
 EXPORTED = ("frnnt_workspace_size", "frnnt_fwd_bwd", "frnnt_error_string", "frnnt_version", "frnnt_profile",
-            "frnnt_profile_read", "frnnt_fwd_bwd_noalloc", "frnnt_fwd_bwd_pruned", "frnnt_fwd_bwd_tdt")
+            "frnnt_profile_read", "frnnt_fwd_bwd_noalloc", "frnnt_fwd_bwd_pruned", "frnnt_fwd_bwd_tdt",
+            "frnnt_token_logprobs", "frnnt_token_logprobs_bwd", "frnnt_recurrence_fwd", "frnnt_recurrence_bwd",
+            "frnnt_recurrence_step", "frnnt_dropout")
 MAX_DURATIONS = 8
+MAX_TOKENS, MAX_TOP, NO_TOKEN, SCAN_CHUNK = 32, 32, -1, 128
 NOALLOC_MAX_BYTES = 64 * 1024 * 1024
 TEST_HOOKS = ("frnnt_test_gemm_bf16", "frnnt_test_joint_variant", "frnnt_test_lose_gemm_loads")
 
@@ -36,6 +39,27 @@ class Dims(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("mode", ctypes.c_int), ("path", ctypes.c_int),
                 ("chunk_cells", ctypes.c_int), ("loss", ctypes.c_int), ("prune_S", ctypes.c_int),
                 ("n_dur", ctypes.c_int), ("durations", ctypes.c_int * 8), ("wgrad_f32", ctypes.c_int)]
+
+
+class LogprobDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("V", ctypes.c_int), ("K", ctypes.c_int), ("top", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("ld", ctypes.c_longlong), ("ldd", ctypes.c_longlong)]
+
+
+class RecurrenceDims(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int) for k in ("B", "T", "D", "dtype")] +
+                [(f"{k}_{s}", ctypes.c_longlong) for k in ("x", "gate", "h", "dh", "dx", "dgate") for s in ("sb", "st")])
+
+
+class StepDims(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int) for k in ("N", "S", "D", "dtype")] +
+                [("x_sn", ctypes.c_longlong), ("gate_sn", ctypes.c_longlong)])
+
+
+class DropoutDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_longlong), ("C", ctypes.c_longlong), ("dtype", ctypes.c_int),
+                ("x_ld", ctypes.c_longlong), ("y_ld", ctypes.c_longlong), ("p", ctypes.c_float),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 class StageStat(ctypes.Structure):
@@ -53,7 +77,8 @@ class FrnntStatusError(RuntimeError):
     def __init__(self, bits: int):
         names = [n for n, v in (("invalid lengths", STATUS_LENGTH), ("invalid labels", STATUS_LABEL),
                                 ("a bounded device wait timed out", STATUS_TIMEOUT),
-                                ("invalid pruning bounds", STATUS_BOUNDS))
+                                ("invalid pruning bounds", STATUS_BOUNDS),
+                                ("invalid parent rows", STATUS_INDEX))
                  if bits & v]
         super().__init__(f"frnnt device status {bits}: {'; '.join(names)}")
         self.bits = bits
@@ -92,6 +117,15 @@ def lib() -> ctypes.CDLL:
         L.frnnt_profile.restype = ctypes.c_int
         L.frnnt_profile_read.argtypes = [ctypes.POINTER(StageStat), ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
         L.frnnt_profile_read.restype = ctypes.c_int
+        L.frnnt_token_logprobs.argtypes = [ctypes.POINTER(LogprobDims)] + [vp] * 9
+        L.frnnt_token_logprobs_bwd.argtypes = [ctypes.POINTER(LogprobDims)] + [vp] * 11
+        L.frnnt_recurrence_fwd.argtypes = [ctypes.POINTER(RecurrenceDims)] + [vp] * 9
+        L.frnnt_recurrence_bwd.argtypes = [ctypes.POINTER(RecurrenceDims)] + [vp] * 11
+        L.frnnt_recurrence_step.argtypes = [ctypes.POINTER(StepDims)] + [vp] * 9
+        L.frnnt_dropout.argtypes = [ctypes.POINTER(DropoutDims)] + [vp] * 4
+        for name in ("frnnt_token_logprobs", "frnnt_token_logprobs_bwd", "frnnt_recurrence_fwd",
+                     "frnnt_recurrence_bwd", "frnnt_recurrence_step", "frnnt_dropout"):
+            getattr(L, name).restype = ctypes.c_int
         L.frnnt_test_gemm_bf16.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int,
                                            ctypes.c_longlong, vp, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
                                            ctypes.c_int, vp, ctypes.c_longlong, ctypes.c_int, vp, vp]
@@ -411,3 +445,385 @@ def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durati
         if bits:
             raise FrnntStatusError(bits)
     return out.loss, out.grads()
+
+
+# ------------------------------------------------------------------ operators beside the loss (include/frnnt_ops.h)
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _float_type(name, t):
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}") from None
+
+
+def _expect(name, t, shape, dtype, dense=True):
+    """Refuses a tensor of another shape, type or (``dense``) layout than the call needs."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(name, t):
+    """Elements from one row of a [N, C] tensor to the next (its columns must be adjacent)."""
+    N, C = t.shape
+    if C > 1 and t.stride(1) != 1:
+        raise ValueError(f"the columns of {name} must be adjacent (stride 1)")
+    return t.stride(0) if N > 1 else max(C, t.stride(0))
+
+
+def _steps(name, t):
+    """(sequence stride, step stride) of a [B, T, D] tensor (its channels must be adjacent)."""
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the channels of {name} must be adjacent (stride 1)")
+    return t.stride(0), t.stride(1)
+
+
+def _on_device(first, others):
+    """Every tensor on the CUDA device of ``first``; run after the shape checks."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("the library computes on the GPU: pass CUDA tensors")
+    for name, t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
+    return dev
+
+
+class _Queue:
+    """The stream a call is queued on, with its device (and, for a stream other
+    than the current one, that stream) current while outputs are allocated and
+    the call is made, so that both belong to the device and stream they are
+    used on."""
+
+    def __init__(self, dev, stream):
+        self.guards = []
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self.guards.append(torch.cuda.device(dev))
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the call's tensors on {dev}")
+            self.guards.append(torch.cuda.stream(stream))
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _status(check, dev):
+    return torch.zeros(1, dtype=torch.int32, device=dev) if check else None
+
+
+def _finish(rc, status):
+    if rc != OK:
+        raise FrnntError(rc, error_string(rc))
+    if status is not None:
+        bits = int(status.item())
+        if bits:
+            raise FrnntStatusError(bits)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class LogProbs:
+    """Outputs of token_logprobs: logp [N, K], entropy [N], lse [N], top_logp
+    [N, top] (fp32) and top_ids [N, top] (int32); logp is None without tokens,
+    the last two are None with top = 0."""
+    __slots__ = ("logp", "entropy", "lse", "top_logp", "top_ids")
+
+    def __init__(self, N, K, top, device):
+        f32 = torch.float32
+        self.logp = torch.empty((N, K), dtype=f32, device=device) if K else None
+        self.entropy = torch.empty(N, dtype=f32, device=device)
+        self.lse = torch.empty(N, dtype=f32, device=device)
+        self.top_logp = torch.empty((N, top), dtype=f32, device=device) if top else None
+        self.top_ids = torch.empty((N, top), dtype=torch.int32, device=device) if top else None
+
+
+def _check_logprobs(logits, tokens, top):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, V]")
+    dt = _float_type("logits", logits)
+    N, V = logits.shape
+    K = 0
+    if tokens is not None:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [N, K]")
+        K = tokens.shape[1]
+        _expect("tokens", tokens, (N, K), torch.int32)
+    if not 0 <= top <= min(V, MAX_TOP) or K > MAX_TOKENS:
+        raise ValueError(f"at most {MAX_TOKENS} tokens and min(V, {MAX_TOP}) alternatives per row")
+    return dt, N, V, K
+
+
+def _check_result(fwd, N, K, top):
+    f32 = torch.float32
+    for name, t, shape, dt in (("logp", fwd.logp, (N, K), f32), ("entropy", fwd.entropy, (N,), f32),
+                               ("lse", fwd.lse, (N,), f32), ("top_logp", fwd.top_logp, (N, top), f32),
+                               ("top_ids", fwd.top_ids, (N, top), torch.int32)):
+        if t is None:
+            if shape[-1] and len(shape) == 2:
+                raise ValueError(f"the result has no {name}")
+        else:
+            _expect(name, t, shape, dt)
+
+
+def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, check=True, stream=None) -> LogProbs:
+    """frnnt_token_logprobs: of each row of logits [N, V] (float32 or bfloat16;
+    rows may be strided), the log-probabilities of its given tokens (int32
+    [N, K]; NO_TOKEN = none), its entropy and log-sum-exp, and its ``top``
+    largest log-probabilities with their columns (ties: lowest column first).
+    -inf logits have probability 0.  ``out``: an earlier call's result, written
+    again.  With ``check`` the device status is read back (which synchronises)
+    and tokens outside [0, V) raise FrnntStatusError."""
+    dt, N, V, K = _check_logprobs(logits, tokens, top)
+    ld = _rows("logits", logits)
+    if out is not None:
+        _check_result(out, N, K, top)
+    dev = _on_device(logits, (("tokens", tokens),) if out is None else
+                     (("tokens", tokens), ("out", out.logp), ("out", out.entropy), ("out", out.lse),
+                      ("out", out.top_logp), ("out", out.top_ids)))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            out = LogProbs(N, K, top, dev)
+        status = _status(check, dev)
+        rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V), logits.data_ptr(), _at(tokens),
+                                        _at(out.logp), out.entropy.data_ptr(), out.lse.data_ptr(), _at(out.top_logp),
+                                        _at(out.top_ids), _at(status), q.handle)
+        _finish(rc, status)
+    return out
+
+
+def token_logprobs_bwd(logits, tokens, fwd: LogProbs, dlogp=None, dentropy=None, dtop=None, out=None, check=True,
+                       stream=None):
+    """frnnt_token_logprobs_bwd: the gradient of sum(logp * dlogp) +
+    sum(entropy * dentropy) + sum(top_logp * dtop) for the logits, in their
+    type.  ``fwd`` is the forward call's result on the same logits and tokens;
+    each of dlogp [N, K], dentropy [N] and dtop [N, top] (fp32) may be None.
+    ``out`` [N, V] may be ``logits`` itself (written in place)."""
+    top = 0 if fwd.top_ids is None else fwd.top_ids.shape[-1]
+    dt, N, V, K = _check_logprobs(logits, tokens, top)
+    ld = _rows("logits", logits)
+    _check_result(fwd, N, K, top)
+    for name, t, shape in (("dlogp", dlogp, (N, K)), ("dentropy", dentropy, (N,)), ("dtop", dtop, (N, top))):
+        if t is not None:
+            _expect(name, t, shape, torch.float32)
+    if out is not None:
+        _expect("out", out, (N, V), logits.dtype, dense=False)
+    dev = _on_device(logits, (("tokens", tokens), ("fwd", fwd.lse), ("fwd", fwd.entropy), ("fwd", fwd.top_ids),
+                              ("dlogp", dlogp), ("dentropy", dentropy), ("dtop", dtop), ("out", out)))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        status = _status(check, dev)
+        rc = lib().frnnt_token_logprobs_bwd(LogprobDims(N, V, K, top, dt, ld, _rows("out", out)), logits.data_ptr(),
+                                            _at(tokens), fwd.lse.data_ptr(), fwd.entropy.data_ptr(), _at(fwd.top_ids),
+                                            _at(dlogp), _at(dentropy), _at(dtop), out.data_ptr(), _at(status),
+                                            q.handle)
+        _finish(rc, status)
+    return out
+
+
+class Recurrence:
+    """Outputs of recurrence: h [B, T, D], h_last [B, D] (fp32) and, for the
+    backward call, the states saved every SCAN_CHUNK steps (fp32)."""
+    __slots__ = ("h", "h_last", "saved")
+
+    def __init__(self, B, T, D, dtype, device, save=True):
+        self.h = torch.empty((B, T, D), dtype=dtype, device=device)
+        self.h_last = torch.empty((B, D), dtype=torch.float32, device=device)
+        n = (T + SCAN_CHUNK - 1) // SCAN_CHUNK
+        self.saved = torch.empty((B, n, D), dtype=torch.float32, device=device) if save else None
+
+
+def _check_recurrence(x, gate, lengths):
+    if x.dim() != 3:
+        raise ValueError("x and gate must be [B, T, D]")
+    dt = _float_type("x", x)
+    _expect("gate", gate, x.shape, x.dtype, dense=False)
+    B, T, D = x.shape
+    if lengths is not None:
+        _expect("lengths", lengths, (B,), torch.int32)
+    return dt, B, T, D
+
+
+def recurrence(x, gate, lengths=None, h0=None, save=True, out: Recurrence | None = None, check=True,
+               stream=None) -> Recurrence:
+    """frnnt_recurrence_fwd: h_t = a_t h_{t-1} + (1 - a_t) x_t with a =
+    sigmoid(gate), over x and gate [B, T, D] (float32 or bfloat16; sequences
+    and steps may be strided, as the halves of one projection are), from h0
+    [B, D] (fp32; zero when None), each sequence to its length (int32 [B]; T
+    when None; rows past it come back 0).  ``save`` keeps what recurrence_bwd
+    needs."""
+    dt, B, T, D = _check_recurrence(x, gate, lengths)
+    if h0 is not None:
+        _expect("h0", h0, (B, D), torch.float32)
+    if out is not None:
+        _expect("out.h", out.h, x.shape, x.dtype, dense=False)
+        _expect("out.h_last", out.h_last, (B, D), torch.float32)
+        if out.saved is not None:
+            _expect("out.saved", out.saved, (B, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, D), torch.float32)
+    strides = _steps("x", x) + _steps("gate", gate)
+    others = (("gate", gate), ("lengths", lengths), ("h0", h0))
+    dev = _on_device(x, others if out is None else others + (("out", out.h), ("out", out.h_last), ("out", out.saved)))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            out = Recurrence(B, T, D, x.dtype, dev, save)
+        status = _status(check and lengths is not None, dev)
+        rc = lib().frnnt_recurrence_fwd(RecurrenceDims(B, T, D, dt, *strides, *_steps("out.h", out.h)), x.data_ptr(),
+                                        gate.data_ptr(), _at(lengths), _at(h0), out.h.data_ptr(),
+                                        out.h_last.data_ptr(), _at(out.saved), _at(status), q.handle)
+        _finish(rc, status)
+    return out
+
+
+def recurrence_bwd(x, gate, fwd: Recurrence, dh, lengths=None, dh_last=None, out: dict | None = None, check=True,
+                   stream=None) -> dict:
+    """frnnt_recurrence_bwd: the gradients dx, dgate [B, T, D] (type of x) and
+    dh0 [B, D] (fp32) of sum(h * dh) + sum(h_last * dh_last).  ``fwd`` is the
+    forward call's result (only its saved states are read) on the same x, gate
+    and lengths.  ``out``: a dict with dx, dgate and dh0 to write to (dx and
+    dgate may be the halves of one gradient)."""
+    dt, B, T, D = _check_recurrence(x, gate, lengths)
+    if fwd.saved is None:
+        raise ValueError("the forward call kept no states (save=False)")
+    _expect("fwd.saved", fwd.saved, (B, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, D), torch.float32)
+    _expect("dh", dh, x.shape, x.dtype, dense=False)
+    if dh_last is not None:
+        _expect("dh_last", dh_last, (B, D), torch.float32)
+    if out is not None:
+        _expect("out dx", out["dx"], x.shape, x.dtype, dense=False)
+        _expect("out dgate", out["dgate"], x.shape, x.dtype, dense=False)
+        _expect("out dh0", out["dh0"], (B, D), torch.float32)
+    strides = _steps("x", x) + _steps("gate", gate) + (0, 0) + _steps("dh", dh)
+    others = (("gate", gate), ("lengths", lengths), ("fwd", fwd.saved), ("dh", dh), ("dh_last", dh_last))
+    dev = _on_device(x, others if out is None else others + tuple(("out", t) for t in out.values()))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            out = dict(dx=torch.empty((B, T, D), dtype=x.dtype, device=dev),
+                       dgate=torch.empty((B, T, D), dtype=x.dtype, device=dev),
+                       dh0=torch.empty((B, D), dtype=torch.float32, device=dev))
+        status = _status(check and lengths is not None, dev)
+        dims = RecurrenceDims(B, T, D, dt, *strides, *_steps("out dx", out["dx"]), *_steps("out dgate", out["dgate"]))
+        rc = lib().frnnt_recurrence_bwd(dims, x.data_ptr(), gate.data_ptr(), _at(lengths), fwd.saved.data_ptr(),
+                                        dh.data_ptr(), _at(dh_last), out["dx"].data_ptr(), out["dgate"].data_ptr(),
+                                        out["dh0"].data_ptr(), _at(status), q.handle)
+        _finish(rc, status)
+    return out
+
+
+def recurrence_step(x, gate, state, parent=None, advance=None, out=None, check=True, stream=None):
+    """frnnt_recurrence_step: one step of N hypotheses.  Row n of x and gate [N,
+    D] continues row parent[n] of state [S, D] (fp32; row n when parent is
+    None), or only copies it where advance[n] (bool) is False.  Returns (h [N,
+    D] in the type of x, new state [N, D] fp32); ``out``: that pair to write
+    to.  The new state may be written over ``state`` when parent is None."""
+    if x.dim() != 2 or state.dim() != 2:
+        raise ValueError("x and gate must be [N, D] and state [S, D]")
+    dt = _float_type("x", x)
+    _expect("gate", gate, x.shape, x.dtype, dense=False)
+    N, D = x.shape
+    S = state.shape[0]
+    _expect("state", state, (S, D), torch.float32)
+    if parent is not None:
+        _expect("parent", parent, (N,), torch.int32)
+    elif N > S:
+        raise ValueError(f"{N} rows need parents among the {S} rows of state")
+    if advance is not None:
+        _expect("advance", advance, (N,), torch.bool)
+    x_sn, gate_sn = _rows("x", x), _rows("gate", gate)
+    h = new = None
+    if out is not None:
+        h, new = out
+        _expect("out h", h, (N, D), x.dtype)
+        _expect("out state", new, (N, D), torch.float32)
+        if parent is not None or new.data_ptr() != state.data_ptr():
+            lo, hi = state.data_ptr(), state.data_ptr() + S * D * 4
+            if new.data_ptr() < hi and lo < new.data_ptr() + N * D * 4:
+                raise ValueError("the new state overlaps the old one, which other rows still read")
+    dev = _on_device(x, (("gate", gate), ("state", state), ("parent", parent), ("advance", advance), ("out", h),
+                         ("out", new)))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            h = torch.empty((N, D), dtype=x.dtype, device=dev)
+            new = torch.empty((N, D), dtype=torch.float32, device=dev)
+        status = _status(check and parent is not None, dev)
+        rc = lib().frnnt_recurrence_step(StepDims(N, S, D, dt, x_sn, gate_sn), x.data_ptr(), gate.data_ptr(),
+                                         state.data_ptr(), _at(parent), _at(advance), h.data_ptr(), new.data_ptr(),
+                                         _at(status), q.handle)
+        _finish(rc, status)
+    return h, new
+
+
+def _matrix(name, t):
+    """(rows, elements per row, row stride) of a tensor whose elements, in
+    row-major order, are rows at one constant distance."""
+    if t.is_contiguous():
+        n = t.numel()
+        return 1, n, n
+    C = t.shape[-1]
+    if t.stride(-1) == 1 or C == 1:
+        if t.dim() == 2:
+            return t.shape[0], C, t.stride(0)
+        try:
+            v = t.view(-1, C)
+        except RuntimeError:
+            pass
+        else:
+            return v.shape[0], C, v.stride(0)
+    raise ValueError(f"{name} must be contiguous, or rows at a constant distance")
+
+
+def dropout(x, p, seed, offset=0, out=None, stream=None):
+    """frnnt_dropout: x with each element dropped with probability p (0 .. 1)
+    and the others scaled by 1 / (1 - p); float32 or bfloat16, any shape.  The
+    mask depends on (seed, offset) and the element's row-major index alone, so
+    the same call on the gradient is the backward pass.  One call uses
+    ceil(numel / 8) counters from ``offset`` on.  ``seed``: an int, or an int64
+    CUDA tensor (seed, offset) read on the device, whose second value is added
+    to ``offset`` (a captured graph then draws new numbers at each replay).
+    ``out`` may be x."""
+    dt = _float_type("x", x)
+    if x.numel() == 0:
+        raise ValueError("x has no elements")
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1], not {p}")
+    rng = None
+    if isinstance(seed, torch.Tensor):
+        rng, seed = seed, 0
+        _expect("seed", rng, (2,), torch.int64)
+    R, C, x_ld = _matrix("x", x)
+    y_ld = C
+    if out is not None:
+        _expect("out", out, x.shape, x.dtype, dense=False)
+        Ry, Cy, y_ld = _matrix("out", out)
+        if (R, C) != (Ry, Cy):     # one of the two is contiguous: take the rows of the other
+            if R == 1:
+                R, C, x_ld = Ry, Cy, Cy
+            elif Ry == 1:
+                y_ld = C
+            else:
+                raise ValueError("x and out have rows of different lengths")
+    dev = _on_device(x, (("seed", rng), ("out", out)))
+    with _Queue(dev, stream) as q:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        mask = (1 << 64) - 1
+        rc = lib().frnnt_dropout(DropoutDims(R, C, dt, x_ld, y_ld, p, seed & mask, offset & mask), x.data_ptr(),
+                                 out.data_ptr(), _at(rng), q.handle)
+        _finish(rc, None)
+    return out

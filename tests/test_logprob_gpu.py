@@ -1,0 +1,248 @@
+"""Token log-probabilities on the GPU against their fp64 oracle: values,
+entropy, alternatives and the gradient of the logits, over types, row lengths
+and layouts, with masked, empty, tied, NaN and infinite rows."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import ops_oracle as O
+from rnn_joint_network_02_b200 import frnnt
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def make(N, V, K, top, dtype, seed=0, pad=0, shift=0, special=True):
+    """Rows of logits on the device (a view `shift` elements into rows of V +
+    pad), tokens, and gradients of the outputs."""
+    g = torch.Generator().manual_seed(seed * 1000 + N * 7 + V)
+    z = torch.randn(N, V, generator=g) * 3
+    z[torch.rand(N, V, generator=g) < 0.2] = -float("inf")
+    if special and N > 4:
+        z[0] = -float("inf")                                  # nothing left
+        z[1] = 1.5                                            # all equal
+        z[2, V // 2] = float("nan")
+        z[3, V - 1] = float("inf")
+        z[4] = -float("inf")
+        z[4, V // 3] = -60000.0                               # one candidate, far down
+    if special and N > 6:
+        z[5] = torch.finfo(TYPES[dtype]).min                  # masked by the type's lowest value, but for one
+        z[5, 0] = 2.0
+        z[6] = z[6].nan_to_num(neginf=-1.0).round()           # many ties
+    wide = torch.full((N, V + pad + shift), 777.0).to(TYPES[dtype])
+    wide[:, shift:shift + V] = z.to(TYPES[dtype])
+    z = wide.cuda()[:, shift:shift + V]
+    tokens = None
+    if K:
+        tokens = torch.randint(0, V, (N, K), generator=g, dtype=torch.int32)
+        tokens[torch.rand(N, K, generator=g) < 0.15] = frnnt.NO_TOKEN
+        if K > 1:
+            tokens[::3, 1] = tokens[::3, 0]                   # the same token twice
+        tokens = tokens.cuda()
+    d = dict(dlogp=torch.randn(N, K, generator=g).cuda() if K else None, dentropy=torch.randn(N, generator=g).cuda(),
+             dtop=torch.randn(N, top, generator=g).cuda() if top else None)
+    return z, tokens, d
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def ints(t):
+    return None if t is None else t.cpu().numpy()
+
+
+def close(got, want, tol, what):
+    got = host(got)
+    assert got.shape == want.shape, what
+    assert np.array_equal(np.isnan(got), np.isnan(want)), f"{what}: NaN in other places"
+    same = (got == want) | np.isnan(want)
+    with np.errstate(invalid="ignore"):
+        bad = ~same & ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} values off, the first at {np.argwhere(bad)[0]}: " \
+                          f"{got[bad][0]!r} for {want[bad][0]!r} +- {np.broadcast_to(tol, want.shape)[bad][0]!r}"
+
+
+def check_forward(z, tokens, top, r):
+    ref = O.token_logprobs(host(z), ints(tokens), top)
+    close(r.lse, ref["lse"], ref["lse_tol"], "lse")
+    close(r.entropy, ref["entropy"], ref["entropy_tol"], "entropy")
+    if tokens is not None:
+        close(r.logp, ref["logp"], ref["logp_tol"], "logp")
+    if top:
+        assert np.array_equal(ints(r.top_ids), ref["top_ids"])
+        close(r.top_logp, ref["top_logp"], ref["top_tol"], "top_logp")
+    return ref
+
+
+def check_backward(z, tokens, ref, d, dz, dtype):
+    want, tol = O.token_logprobs_bwd(host(z), ints(tokens), ref, host(d["dlogp"]), host(d["dentropy"]),
+                                     host(d["dtop"]), dtype)
+    close(dz, want, tol, "dlogits")
+
+
+SHAPES = [
+    # N, V, K, top
+    (9, 1, 1, 1), (9, 2, 2, 2), (9, 7, 1, 7), (9, 8, 2, 4), (9, 31, 3, 5), (9, 33, 1, 32), (9, 128, 2, 1),
+    (9, 255, 0, 8), (9, 257, 2, 0), (9, 1000, 4, 20), (9, 1024, 2, 8), (9, 1025, 32, 32), (40, 1024, 2, 0),
+    (1, 1024, 1, 8), (7, 4096, 1, 16), (7, 4099, 2, 3), (3, 50257, 1, 20), (2, 131071, 2, 32), (1, 131072, 1, 4),
+    (700, 130, 2, 4), (2500, 24, 1, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K,top", SHAPES)
+def test_forward_and_backward(cuda_ok, N, V, K, top, dtype):
+    z, tokens, d = make(N, V, K, top, dtype)
+    r = frnnt.token_logprobs(z, tokens, top=top)
+    ref = check_forward(z, tokens, top, r)
+    dz = frnnt.token_logprobs_bwd(z, tokens, r, **d)
+    check_backward(z, tokens, ref, d, dz, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,shift,out_pad,out_shift", [(8, 0, 8, 0), (3, 0, 0, 0), (0, 1, 0, 0), (1, 2, 5, 3),
+                                                         (24, 5, 24, 5), (0, 0, 1, 0)])
+@pytest.mark.parametrize("V", [9, 1024, 2051])
+def test_strided_and_unaligned_rows(cuda_ok, V, pad, shift, out_pad, out_shift, dtype):
+    """Rows at any distance and alignment; elements around the output rows stay."""
+    N, K, top = 8, 2, 5
+    z, tokens, d = make(N, V, K, top, dtype, seed=3, pad=pad, shift=shift)
+    r = frnnt.token_logprobs(z, tokens, top=min(top, V))
+    ref = check_forward(z, tokens, top, r)
+    wide = torch.full((N, out_shift + V + out_pad), 5.0, dtype=z.dtype, device="cuda")
+    out = wide[:, out_shift:out_shift + V]
+    dz = frnnt.token_logprobs_bwd(z, tokens, r, **d, out=out)
+    assert dz.data_ptr() == out.data_ptr()
+    check_backward(z, tokens, ref, d, out, dtype)
+    assert bool((wide[:, :out_shift] == 5).all()) and bool((wide[:, out_shift + V:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("terms", [("dlogp",), ("dentropy",), ("dtop",), ("dlogp", "dtop"), ()])
+def test_backward_terms_one_by_one(cuda_ok, terms, dtype):
+    z, tokens, d = make(12, 300, 2, 4, dtype, seed=5)
+    d = {k: (v if k in terms else None) for k, v in d.items()}
+    r = frnnt.token_logprobs(z, tokens, top=4)
+    ref = O.token_logprobs(host(z), ints(tokens), 4)
+    check_backward(z, tokens, ref, d, frnnt.token_logprobs_bwd(z, tokens, r, **d), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,pad", [(1024, 0), (20001, 7)])
+def test_backward_in_place(cuda_ok, V, pad, dtype):
+    z, tokens, d = make(10, V, 3, 6, dtype, seed=6, pad=pad)
+    r = frnnt.token_logprobs(z, tokens, top=6)
+    apart = frnnt.token_logprobs_bwd(z, tokens, r, **d)
+    frnnt.token_logprobs_bwd(z, tokens, r, **d, out=z)
+    assert torch.equal(apart.nan_to_num(nan=-99.0), z.nan_to_num(nan=-99.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V", [(3, 70000), (300, 1024)])
+def test_same_bits_every_time(cuda_ok, N, V, dtype):
+    z, tokens, d = make(N, V, 4, 8, dtype, seed=7)
+    first = None
+    for _ in range(3):
+        r = frnnt.token_logprobs(z, tokens, top=8)
+        dz = frnnt.token_logprobs_bwd(z, tokens, r, **d)
+        bits = [t.contiguous().view(torch.uint8).clone() for t in (r.logp, r.entropy, r.lse, r.top_logp, r.top_ids, dz)]
+        first = first or bits
+        assert all(torch.equal(a, b) for a, b in zip(first, bits))
+
+
+@pytest.mark.parametrize("bad", [-2, 300, 2 ** 31 - 1])
+def test_bad_tokens_raise_and_touch_nothing_else(cuda_ok, bad):
+    z, tokens, d = make(6, 300, 2, 0, "f32", special=False)
+    good = frnnt.token_logprobs(z, tokens)
+    wrong = tokens.clone()
+    wrong[4, 1] = bad
+    with pytest.raises(frnnt.FrnntStatusError) as e:
+        frnnt.token_logprobs(z, wrong)
+    assert e.value.bits == frnnt.STATUS_LABEL
+    r = frnnt.token_logprobs(z, wrong, check=False)
+    rows = [0, 1, 2, 3, 5]
+    assert torch.equal(r.logp[rows], good.logp[rows]) and torch.equal(r.entropy, good.entropy)
+    with pytest.raises(frnnt.FrnntStatusError):
+        frnnt.token_logprobs_bwd(z, wrong, good, dlogp=d["dlogp"])
+
+
+def test_offsets_past_32_bits(cuda_ok):
+    """Rows that start more than 2^32 bytes (and 2^31 elements) into the array."""
+    V, ld = 1000, 1_100_000_000
+    z, tokens, d = make(3, V, 1, 4, "bf16", special=False)
+    big = torch.empty(2 * ld + V, dtype=torch.bfloat16, device="cuda")
+    far = big.as_strided((3, V), (ld, 1))
+    far.copy_(z)
+    a, b = frnnt.token_logprobs(z, tokens, top=4), frnnt.token_logprobs(far, tokens, top=4)
+    assert torch.equal(a.logp, b.logp) and torch.equal(a.top_ids, b.top_ids) and torch.equal(a.entropy, b.entropy)
+    want = frnnt.token_logprobs_bwd(z, tokens, a, **d)
+    frnnt.token_logprobs_bwd(far, tokens, a, **d, out=far)
+    assert torch.equal(want, far)
+
+
+def test_result_used_again_and_other_stream(cuda_ok):
+    z, tokens, _ = make(20, 512, 2, 4, "bf16", seed=8)
+    want = frnnt.token_logprobs(z, tokens, top=4)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    r = frnnt.token_logprobs(z, tokens, top=4, stream=side)
+    again = frnnt.token_logprobs(z, tokens, top=4, out=r, stream=side)
+    side.synchronize()
+    assert again is r
+    assert torch.equal(r.top_ids, want.top_ids) and torch.equal(r.logp.nan_to_num(), want.logp.nan_to_num())
+
+
+def test_captured_and_replayed(cuda_ok):
+    """Two captured graphs and an eager call share nothing but their inputs."""
+    z, tokens, d = make(16, 40000, 2, 8, "bf16", seed=9, special=False)
+    other = make(16, 40000, 2, 8, "bf16", seed=10, special=False)[0]
+    want = [(r.logp.clone(), r.top_ids.clone(), frnnt.token_logprobs_bwd(t, tokens, r, **d))
+            for t in (z, other) for r in [frnnt.token_logprobs(t, tokens, top=8)]]
+    buf, graphs, outs = [z.clone(), z.clone()], [], []
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for i in range(2):
+            stream.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                r = frnnt.token_logprobs(buf[i], tokens, top=8, check=False)
+                dz = frnnt.token_logprobs_bwd(buf[i], tokens, r, **d, check=False)
+            graphs.append(g)
+            outs.append((r.logp, r.top_ids, dz))
+        buf[1].copy_(other)
+        for g in (graphs[0], graphs[1], graphs[0]):
+            g.replay()
+        stream.synchronize()
+    for got, ref in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_two_threads(cuda_ok):
+    cases = [make(30, 5000, 2, 8, "bf16", seed=s, special=False) for s in (11, 12)]
+    want = [frnnt.token_logprobs(z, t, top=8) for z, t, _ in cases]
+    torch.cuda.synchronize()
+    got, errors, start = [None, None], [], threading.Barrier(2)
+
+    def worker(i):
+        try:
+            s = torch.cuda.Stream()
+            start.wait()
+            for _ in range(20):
+                r = frnnt.token_logprobs(cases[i][0], cases[i][1], top=8, stream=s)
+            s.synchronize()
+            got[i] = r
+        except Exception as e:   # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not errors and all(g is not None for g in got), errors
+    for g, w in zip(got, want):
+        assert torch.equal(g.logp, w.logp) and torch.equal(g.top_ids, w.top_ids)
