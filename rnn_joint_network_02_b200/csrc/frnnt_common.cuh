@@ -60,6 +60,20 @@ __device__ __forceinline__ float log_add_exp(float a, float b) {
   return m == -INFINITY ? m : r;
 }
 
+// Cluster barrier (release / acquire at cluster scope), in two halves: every
+// thread of every block of the cluster makes both.  A block's shared memory may
+// be written by the others only after a barrier that it took part in, and each
+// such write must be followed by one before the block may exit.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address of p's place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cluster(const void* p, int rank) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
 template <typename T> __device__ __forceinline__ float to_f32(T x);
 template <> __device__ __forceinline__ float to_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }

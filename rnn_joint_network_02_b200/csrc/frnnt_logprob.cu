@@ -7,126 +7,539 @@
 namespace frnnt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
+constexpr int kWarps = 8;    // warps of a block
+constexpr int kVecs = 4;     // 16-byte vectors a lane holds at a time: a warp takes 2 KB of a row at once
+constexpr unsigned kAll = 0xFFFFFFFFu;
+// Exponents are held above this: 2^-160 is 0 in fp32, and 0 times it is 0, where 0 times -inf (a forbidden entry's)
+// would be NaN.
+constexpr float kFloor = -160.f;
 
-// Order-preserving image of a float among unsigned integers; NaN below all.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0u;
-  if (v == 0.f) v = 0.f;   // -0 and +0 are equal
-  const uint32_t b = __float_as_uint(v);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+// ------------------------------------------------------------------ arithmetic on pairs
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-
-template <typename F>
-__device__ __forceinline__ float block_reduce(float v, float* sm, F f) {
-  sm[threadIdx.x] = v;
-  __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) sm[threadIdx.x] = f(sm[threadIdx.x], sm[threadIdx.x + o]);
-    __syncthreads();
-  }
-  const float r = sm[0];
-  __syncthreads();
+__device__ __forceinline__ float2 open(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float at_least(float x, float lo) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
   return r;
 }
 
-// A block per row; one pass for the maximum, one for the sums, one for each
-// alternative.
+// ------------------------------------------------------------------ rows
+// A row as 16-byte vectors between an unaligned head and a tail, each shorter
+// than a vector.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(int V, int K, int top, long long ld, const T* logits,
-                                                               const int32_t* tokens, float* logp, float* entropy,
-                                                               float* lse, float* top_logp, int32_t* top_ids,
-                                                               int32_t* status) {
-  __shared__ float sm[kThreads];
-  __shared__ unsigned long long best_sm[kThreads];
-  const long long n = blockIdx.x;
-  const T* z = logits + n * ld;
-  float m = -INFINITY;
-  for (int j = threadIdx.x; j < V; j += kThreads) m = fmaxf(m, to_f32<T>(z[j]));
-  m = block_reduce(m, sm, [](float a, float b) { return fmaxf(a, b); });
-  const float m0 = m == -INFINITY ? 0.f : m;
-  float s = 0.f, w = 0.f;
-  for (int j = threadIdx.x; j < V; j += kThreads) {
-    const float d = to_f32<T>(z[j]) - m0, e = expf(d);
-    s += e;
-    if (e != 0.f) w += e * d;
+struct Row {
+  static constexpr int E = 16 / sizeof(T);
+  const T* p;
+  int head, nvec, tail;
+  __device__ __forceinline__ Row(const T* row, int V) : p(row) {
+    const int off = (int)((uintptr_t)row / sizeof(T) % E);
+    head = min(off ? E - off : 0, V);
+    nvec = (V - head) / E;
+    tail = V - head - nvec * E;
   }
-  s = block_reduce(s, sm, [](float a, float b) { return a + b; });
-  w = block_reduce(w, sm, [](float a, float b) { return a + b; });
-  const bool empty = s == 0.f;
-  const float ls = logf(s), l = empty ? -INFINITY : m0 + ls;
-  if (threadIdx.x == 0) {
-    lse[n] = l;
-    entropy[n] = empty ? 0.f : ls - w / s;
+  __device__ __forceinline__ const uint4* vec(int v) const { return reinterpret_cast<const uint4*>(p + head) + v; }
+  // The column of the lane's element of head and tail together, or -1: lanes
+  // 0 .. and lanes 8 ..
+  __device__ __forceinline__ int edge(int lane) const {
+    return lane < 8 ? (lane < head ? lane : -1) : (lane - 8 < tail ? head + nvec * E + lane - 8 : -1);
   }
-  for (int k = threadIdx.x; k < K; k += kThreads) {
-    const int t = tokens[n * K + k];
-    if (t != FRNNT_NO_TOKEN && (t < 0 || t >= V) && status) atomicOr(status, FRNNT_STATUS_LABEL);
-    logp[n * K + k] = t < 0 || t >= V ? 0.f : (empty ? -INFINITY : (to_f32<T>(z[t]) - m0) - ls);
-  }
-  unsigned long long last = ~0ull;
-  for (int i = 0; i < top; ++i) {
-    unsigned long long best = 0;
-    for (int j = threadIdx.x; j < V; j += kThreads) {
-      const unsigned long long c = ((unsigned long long)order_key(to_f32<T>(z[j])) << 32) | (uint32_t)~j;
-      if (c < last && c > best) best = c;
-    }
-    best_sm[threadIdx.x] = best;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-      if (threadIdx.x < o && best_sm[threadIdx.x + o] > best_sm[threadIdx.x])
-        best_sm[threadIdx.x] = best_sm[threadIdx.x + o];
-      __syncthreads();
-    }
-    last = best_sm[0];
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int j = (int)~(uint32_t)last;
-      top_ids[n * top + i] = j;
-      top_logp[n * top + i] = empty ? -INFINITY : (to_f32<T>(z[j]) - m0) - ls;
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 r, float (&f)[16 / sizeof(T)]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(u[i]);
+    } else {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
 }
 
+// ------------------------------------------------------------------ softmax statistics
+// s = sum of 2^d and w = sum of 2^d d over the values seen, with d = (z - m)
+// log2 e and m the largest of them: lse = m + ln s, and the entropy ln s - ln2 w / s.
+struct Stats {
+  float m, s, w;
+};
+
+__device__ __forceinline__ void rescale(Stats& a, float m) {   // to a reference m >= a.m, not -inf
+  const float d = fmaxf((a.m - m) * kLog2e, -1000.f), f = exp2_approx(d);
+  a.w = f * fmaf(d, a.s, a.w);
+  a.s *= f;
+  a.m = m;
+}
+__device__ __forceinline__ void join(Stats& a, Stats b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) {   // neither has a value (or they hold NaN only)
+    a.s += b.s;
+    return;
+  }
+  rescale(a, m);
+  rescale(b, m);
+  a.s += b.s;
+  a.w += b.w;
+}
+__device__ __forceinline__ void join_warp(Stats& a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  if (m > -INFINITY) rescale(a, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(kAll, a.s, o);
+    a.w += __shfl_xor_sync(kAll, a.w, o);
+  }
+}
+
+// ------------------------------------------------------------------ best alternatives
+// Candidates are ordered by one 64-bit number: the value's order-preserving
+// image above the inverted column, so that equal values rank by column, the
+// lowest first.  NaN ranks below everything; 0 is no candidate.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.f);   // -0 becomes +0: they are equal
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+__device__ __forceinline__ uint64_t candidate(float v, int col) { return ((uint64_t)order_key(v) << 32) | (uint32_t)~col; }
+
+// A warp's best `top` so far, in descending order, one a lane.
+struct Best {
+  uint64_t mine = 0;       // this lane's entry
+  float bound = -INFINITY; // the last entry's value once there are `top`: smaller values are no candidates
+  // Takes the candidates of the lanes that offer one (0: none), one after another.
+  __device__ __forceinline__ void offer(uint64_t c, int lane, int top) {
+    unsigned from = __ballot_sync(kAll, c > __shfl_sync(kAll, mine, top - 1));
+    while (from) {
+      const int src = __ffs(from) - 1;
+      from &= from - 1;
+      const uint64_t x = __shfl_sync(kAll, c, src);
+      const int pos = __popc(__ballot_sync(kAll, mine > x));
+      const uint64_t up = __shfl_up_sync(kAll, mine, 1);
+      if (lane >= pos) mine = lane == pos ? x : up;
+    }
+  }
+  __device__ __forceinline__ void settle(int top) {
+    const uint32_t k = (uint32_t)(__shfl_sync(kAll, mine, top - 1) >> 32);
+    bound = k == 0u ? -INFINITY : key_value(k);
+  }
+};
+
+// ------------------------------------------------------------------ forward
+struct FwdParams {
+  int N, V, K, top;
+  long long ld;
+  const int32_t* tokens;
+  float *logp, *entropy, *lse, *top_logp;
+  int32_t *top_ids, *status;
+};
+
+// The share of one warp (number g of G that share the row, 2 KB each in turn):
+// statistics and alternatives in one pass over the vectors.
+template <typename T, bool TOP>
+__device__ __forceinline__ void scan_row(const Row<T>& row, int g, int G, int lane, int top, Stats& st, Best& best) {
+  constexpr int E = Row<T>::E;
+  for (int base = g * 32 * kVecs; base < row.nvec; base += G * 32 * kVecs) {
+    float z[kVecs][E], vmax[kVecs];
+    const int n = min(kVecs, (row.nvec - base + 31) / 32);
+    uint4 raw[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int v = base + u * 32 + lane;
+      const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
+      raw[u] = make_uint4(none, none, none, none);
+      if (v < row.nvec) raw[u] = __ldg(row.vec(v));
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      vmax[u] = -INFINITY;
+      if (u < n) {
+        unpack<T>(raw[u], z[u]);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) vmax[u] = fmaxf(vmax[u], fmaxf(z[u][i], z[u][i + 1]));
+      }
+      m = fmaxf(m, vmax[u]);
+    }
+    const float ref = fmaxf(m, st.m);
+    if (ref > st.m) rescale(st, ref);
+    // a lane that has seen only -inf (or NaN) sums about 0
+    const float at = ref == -INFINITY ? 0.f : -ref;
+    const uint64_t at2 = pair(at, at), l2e = pair(kLog2e, kLog2e);
+    uint64_t s2 = pair(0.f, 0.f), w2 = s2;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (u < n) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const float2 d = open(mul2(add2(pair(z[u][i], z[u][i + 1]), at2), l2e));
+          const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
+          const uint64_t e2 = pair(exp2_approx(d0), exp2_approx(d1));
+          s2 = add2(s2, e2);
+          w2 = fma2(e2, pair(d0, d1), w2);
+        }
+      }
+    const float2 s = open(s2), w = open(w2);
+    st.s += s.x + s.y;
+    st.w += w.x + w.y;
+
+    if constexpr (TOP) {
+      float bound = best.bound;
+      if (bound == -INFINITY) {
+        // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
+        uint32_t k = order_key(m), kth = 0;
+        for (int i = 0; i < top; ++i) {
+          kth = __reduce_max_sync(kAll, k);
+          if (k == kth) k = 0;
+        }
+        if (kth) bound = key_value(kth);
+      }
+      unsigned vecs = 0;
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (base + u * 32 + lane < row.nvec && vmax[u] >= bound) vecs |= 1u << u;
+      if (__any_sync(kAll, vecs)) {
+        while (__any_sync(kAll, vecs)) {
+          // the lane's next vector that may hold candidates, read again (from cache) to be indexed
+          unsigned elems = 0;
+          int col = 0;
+          uint4 r = make_uint4(0, 0, 0, 0);
+          if (vecs) {
+            const int v = base + (__ffs(vecs) - 1) * 32 + lane;
+            vecs &= vecs - 1;
+            r = __ldg(row.vec(v));
+            col = row.head + v * E;
+            float f[E];
+            unpack<T>(r, f);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+              if (!(f[i] < bound)) elems |= 1u << i;
+          }
+          while (__any_sync(kAll, elems)) {
+            uint64_t c = 0;
+            if (elems) {
+              const int i = __ffs(elems) - 1;
+              elems &= elems - 1;
+              const int word = sizeof(T) == 4 ? i : i >> 1;
+              uint32_t x = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
+              if (sizeof(T) == 2) x = (i & 1) ? x & 0xFFFF0000u : x << 16;
+              c = candidate(__uint_as_float(x), col + i);
+            }
+            best.offer(c, lane, top);
+          }
+        }
+        best.settle(top);
+      }
+    }
+  }
+  if (g == 0 && row.head + row.tail > 0) {
+    const int col = row.edge(lane);
+    const float z = col >= 0 ? to_f32<T>(__ldg(row.p + col)) : -INFINITY;
+    const float ref = fmaxf(z, st.m);
+    if (ref > st.m) rescale(st, ref);
+    const float d = at_least((z + (ref == -INFINITY ? 0.f : -ref)) * kLog2e, kFloor), e = exp2_approx(d);
+    st.s += e;
+    st.w = fmaf(e, d, st.w);
+    if constexpr (TOP) best.offer(col >= 0 ? candidate(z, col) : 0, lane, top);
+  }
+}
+
+// What one warp writes for a row from its joined statistics and alternatives.
+template <typename T, bool TOP>
+__device__ __forceinline__ void write_row(const FwdParams& p, long long n, int lane, const Stats& st, const Best& best,
+                                          int token, float zt) {
+  const bool empty = st.s == 0.f;
+  const float ls = logf(st.s);
+  if (lane == 0) {
+    p.lse[n] = empty ? -INFINITY : st.m + ls;
+    p.entropy[n] = empty ? 0.f : fmaf(st.w / st.s, -kLn2, ls);
+  }
+  if (lane < p.K) {
+    const bool given = token >= 0 && token < p.V;
+    if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
+    p.logp[n * p.K + lane] = !given ? 0.f : empty ? -INFINITY : (zt - st.m) - ls;
+  }
+  if (TOP && lane < p.top) {
+    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best.mine;
+    p.top_logp[n * p.top + lane] = empty ? -INFINITY : (key_value((uint32_t)(best.mine >> 32)) - st.m) - ls;
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(int V, int K, int top, long long ld, long long ldd,
-                                                               const T* logits, const int32_t* tokens,
-                                                               const float* lse, const float* entropy,
-                                                               const int32_t* top_ids, const float* dlogp,
-                                                               const float* dentropy, const float* dtop, T* dlogits,
-                                                               int32_t* status) {
-  __shared__ int ids[FRNNT_MAX_TOKENS + FRNNT_MAX_TOP];
-  __shared__ float coef[FRNNT_MAX_TOKENS + FRNNT_MAX_TOP];
-  const long long n = blockIdx.x;
-  const int nk = dlogp ? K : 0, nt = dtop ? top : 0, cnt = nk + nt;
-  for (int i = threadIdx.x; i < cnt; i += kThreads) {
-    int t = i < nk ? tokens[n * K + i] : top_ids[n * top + i - nk];
-    const bool none = i < nk && t == FRNNT_NO_TOKEN;
-    if (!none && (t < 0 || t >= V) && status) atomicOr(status, FRNNT_STATUS_LABEL);
-    if (t < 0 || t >= V) t = -1;
-    ids[i] = t;
-    coef[i] = t < 0 ? 0.f : (i < nk ? dlogp[n * K + i] : dtop[n * top + i - nk]);
+__device__ __forceinline__ void read_token(const FwdParams& p, long long n, const T* row, int lane, int& token, float& zt) {
+  token = FRNNT_NO_TOKEN;
+  zt = 0.f;
+  if (lane < p.K) {
+    token = p.tokens[n * p.K + lane];
+    if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row + token));
   }
-  __syncthreads();
-  float c = 0.f;
-  bool none = !dentropy;   // a row without any term gets zeros, whatever it holds
-  for (int i = 0; i < cnt; ++i) {
-    c += coef[i];
-    none = none && ids[i] < 0;
+}
+
+// A warp a row.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kWarps * 32) logprob_warp_kernel(FwdParams p, const T* __restrict__ logits) {
+  const int lane = threadIdx.x & 31;
+  const long long n = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (n >= p.N) return;
+  const Row<T> row(logits + n * p.ld, p.V);
+  int token;
+  float zt;
+  read_token<T>(p, n, row.p, lane, token, zt);
+  Stats st{-INFINITY, 0.f, 0.f};
+  Best best;
+  scan_row<T, TOP>(row, 0, 1, lane, p.top, st, best);
+  join_warp(st);
+  write_row<T, TOP>(p, n, lane, st, best, token, zt);
+}
+
+// A cluster of CL blocks a row: the warps' statistics and alternatives meet in
+// the shared memory of the first block.
+template <typename T, bool TOP, int CL>
+__global__ void __launch_bounds__(kWarps * 32) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
+  __shared__ Stats stats[kWarps * CL];
+  __shared__ uint64_t lists[TOP ? kWarps * CL : 1][FRNNT_MAX_TOP];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
+  const long long n = blockIdx.x / CL;
+  if (CL > 1) cluster_arrive();
+  const Row<T> row(logits + n * p.ld, p.V);
+  int token = FRNNT_NO_TOKEN;
+  float zt = 0.f;
+  if (g == 0) read_token<T>(p, n, row.p, lane, token, zt);
+  Stats st{-INFINITY, 0.f, 0.f};
+  Best best;
+  scan_row<T, TOP>(row, g, kWarps * CL, lane, p.top, st, best);
+  join_warp(st);
+  if (CL > 1) {
+    cluster_wait();   // the first block runs: its shared memory may be written
+    if (lane == 0) {
+      const uint32_t at = in_cluster(&stats[g], 0);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(st.m) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(st.s) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(st.w) : "memory");
+    }
+    if (TOP && lane < p.top)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&lists[g][lane], 0)), "l"(best.mine) : "memory");
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    if (lane == 0) stats[g] = st;
+    if (TOP && lane < p.top) lists[g][lane] = best.mine;
+    __syncthreads();
   }
-  const float l = lse[n], dh = dentropy ? dentropy[n] : 0.f, h = dentropy ? entropy[n] : 0.f;
-  for (int j = threadIdx.x; j < V; j += kThreads) {
-    const float lp = to_f32<T>(logits[n * ld + j]) - l, p = expf(lp);
-    float g = p == 0.f ? 0.f : -p * (c + dh * (lp + h));
-    for (int i = 0; i < cnt; ++i)
-      if (ids[i] == j) g += coef[i];
-    dlogits[n * ldd + j] = from_f32<T>(none || l == -INFINITY ? 0.f : g);
+  if (g != 0) return;
+  st = lane < kWarps * CL ? stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int k = 32; k < kWarps * CL; k += 32) join(st, stats[k + lane]);
+  join_warp(st);
+  if constexpr (TOP)
+    for (int k = 1; k < kWarps * CL; ++k) best.offer(lane < p.top ? lists[k][lane] : 0, lane, p.top);
+  write_row<T, TOP>(p, n, lane, st, best, token, zt);
+}
+
+// ------------------------------------------------------------------ backward
+struct BwdParams {
+  int N, V, K, top;
+  int segments;            // warps that share a row
+  long long ld, ldd;
+  const int32_t *tokens, *top_ids;
+  const float *lse, *entropy, *dlogp, *dentropy, *dtop;
+  int32_t* status;
+};
+
+constexpr int kSegment = 8 * 32 * kVecs;   // vectors of a row that one warp takes: 16 KB
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)], bool whole) {
+  constexpr int E = 16 / sizeof(T);
+  if (whole) {
+    uint4 r;
+    if constexpr (sizeof(T) == 4) {
+      r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      r = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    *reinterpret_cast<uint4*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) p[i] = from_f32<T>(f[i]);
   }
+}
+
+// dz_j = -p_j (A + B log2 p_j) with A = sum of the coefficients + dentropy
+// entropy and B = dentropy ln2, plus the coefficients of column j: the dense
+// part first, then the few columns that have coefficients are written again
+// by the lanes that hold them.  Every element is read before it is written,
+// by the same warp, so dlogits may be the logits' memory (no non-coherent loads).
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, const T* logits, T* dlogits) {
+  constexpr int E = Row<T>::E;
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long n = unit / p.segments;
+  const int seg = (int)(unit - n * p.segments);
+  if (n >= p.N) return;
+  const Row<T> row(logits + n * p.ld, p.V);
+  T* out = dlogits + n * p.ldd;
+  const int v0 = seg * kSegment, v1 = min(row.nvec, v0 + kSegment);
+
+  // coefficients: slots lane and lane + 32 of the given tokens and the alternatives
+  const int nk = p.dlogp ? p.K : 0, count = nk + (p.dtop ? p.top : 0);
+  int id[2];
+  float coef[2], zt[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 32 * i;
+    id[i] = -1;
+    coef[i] = zt[i] = 0.f;
+    if (k < count) {
+      const int t = k < nk ? p.tokens[n * p.K + k] : p.top_ids[n * p.top + k - nk];
+      if (t >= 0 && t < p.V) {
+        id[i] = t;
+        coef[i] = k < nk ? p.dlogp[n * p.K + k] : p.dtop[n * p.top + k - nk];
+        zt[i] = to_f32<T>(row.p[t]);
+      } else if (!(k < nk && t == FRNNT_NO_TOKEN) && p.status) {
+        atomicOr(p.status, FRNNT_STATUS_LABEL);
+      }
+    }
+  }
+  const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
+  float sum = coef[0] + coef[1];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  float total[2] = {0.f, 0.f};   // of all slots with the same column
+  for (int k = 0; k < count; ++k) {
+    const int t = __shfl_sync(kAll, k < 32 ? id[0] : id[1], k & 31);
+    const float x = __shfl_sync(kAll, k < 32 ? coef[0] : coef[1], k & 31);
+    if (t == id[0]) total[0] += x;
+    if (t == id[1]) total[1] += x;
+  }
+  // a row without any term, or with nothing left by its mask, gets zeros
+  const bool none = l == -INFINITY || (!p.dentropy && !__any_sync(kAll, id[0] >= 0 || id[1] >= 0));
+  const float A = fmaf(de, h, sum), B = de * kLn2;
+  auto dense = [&](float z) {
+    const float d = at_least((z - l) * kLog2e, kFloor);
+    return -exp2_approx(d) * fmaf(B, d, A);
+  };
+  auto patch = [&](int lo, int hi) {   // columns lo .. hi - 1 have been written by this warp
+    __syncwarp();
+    if (!none) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(dense(zt[i]) + total[i]);
+    }
+  };
+
+  const bool whole = ((uintptr_t)(out + row.head) & 15u) == 0;
+  const uint64_t l2 = pair(-l, -l), l2e = pair(kLog2e, kLog2e), A2 = pair(A, A), B2 = pair(B, B);
+  for (int base = v0; base < v1; base += 32 * kVecs) {
+    uint4 raw[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int v = base + u * 32 + lane;
+      if (v < v1) raw[u] = *row.vec(v);
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int v = base + u * 32 + lane;
+      if (v < v1) {
+        float f[E];
+        unpack<T>(raw[u], f);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const float2 d = open(mul2(add2(pair(f[i], f[i + 1]), l2), l2e));
+          const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
+          const float2 g = open(mul2(pair(-exp2_approx(d0), -exp2_approx(d1)), fma2(B2, pair(d0, d1), A2)));
+          f[i] = none ? 0.f : g.x;
+          f[i + 1] = none ? 0.f : g.y;
+        }
+        store_vec<T>(out + row.head + v * E, f, whole);
+      }
+    }
+    patch(row.head + base * E, row.head + min(v1, base + 32 * kVecs) * E);
+  }
+  if (seg == 0 && row.head + row.tail > 0) {
+    const int col = row.edge(lane);
+    if (col >= 0) out[col] = from_f32<T>(none ? 0.f : dense(to_f32<T>(row.p[col])));
+    patch(0, row.head);
+    patch(row.head + row.nvec * E, p.V);
+  }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, bool TOP>
+void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
+  const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
+  const long long chunks = (p.V + chunk - 1) / chunk;
+  if (chunks <= 2 || (chunks <= 4 && p.N >= 148 * 32)) {
+    launch_k(logprob_warp_kernel<T, TOP>, dim3((p.N + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, logits);
+  } else {
+    int cl = 1;
+    while (cl < 8 && (long long)p.N * cl < 148 && chunks > (long long)kWarps * cl) cl *= 2;
+    auto go = [&](auto kernel) { launch_k(kernel, dim3((unsigned)p.N * cl), dim3(kWarps * 32), 0, st, cl, p, logits); };
+    if (cl == 1) go(logprob_block_kernel<T, TOP, 1>);
+    else if (cl == 2) go(logprob_block_kernel<T, TOP, 2>);
+    else if (cl == 4) go(logprob_block_kernel<T, TOP, 4>);
+    else go(logprob_block_kernel<T, TOP, 8>);
+  }
+  note_launch();
+}
+
+template <typename T>
+void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
+  p.segments = (p.V / (int)(16 / sizeof(T)) + kSegment - 1) / kSegment;
+  if (p.segments < 1) p.segments = 1;
+  const long long warps = (long long)p.N * p.segments;
+  launch_k(logprob_bwd_kernel<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, 1, p,
+           logits, dlogits);
+  note_launch();
 }
 
 int check(const frnnt_logprob_dims* d) {
   if (d->dtype != FRNNT_F32 && d->dtype != FRNNT_BF16) return FRNNT_ERR_UNSUPPORTED;
-  if (d->N < 1 || d->V < 1 || d->K < 0 || d->K > FRNNT_MAX_TOKENS || d->top < 0 || d->top > FRNNT_MAX_TOP ||
+  if (d->N < 1 || d->N > (1 << 27) || d->V < 1 || d->V > (1 << 30) || d->K < 0 || d->K > FRNNT_MAX_TOKENS || d->top < 0 || d->top > FRNNT_MAX_TOP ||
       d->top > d->V || d->ld < d->V || d->ld > (1LL << 40))
     return FRNNT_ERR_DIMS;
   return FRNNT_OK;
@@ -152,14 +565,14 @@ extern "C" FRNNT_API int frnnt_token_logprobs(const frnnt_logprob_dims* d, const
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs", st);
-    if (d->dtype == FRNNT_BF16)
-      logprob_fwd_kernel<__nv_bfloat16><<<d->N, kThreads, 0, st>>>(d->V, d->K, d->top, d->ld,
-                                                                   (const __nv_bfloat16*)logits, tokens, logp,
-                                                                   entropy, lse, top_logp, top_ids, status);
-    else
-      logprob_fwd_kernel<float><<<d->N, kThreads, 0, st>>>(d->V, d->K, d->top, d->ld, (const float*)logits, tokens,
-                                                           logp, entropy, lse, top_logp, top_ids, status);
-    note_launch();
+    const FwdParams p{d->N, d->V, d->K, d->top, d->ld, tokens, logp, entropy, lse, top_logp, top_ids, status};
+    if (d->dtype == FRNNT_BF16) {
+      auto* z = (const __nv_bfloat16*)logits;
+      d->top ? launch_fwd<__nv_bfloat16, true>(p, z, st) : launch_fwd<__nv_bfloat16, false>(p, z, st);
+    } else {
+      auto* z = (const float*)logits;
+      d->top ? launch_fwd<float, true>(p, z, st) : launch_fwd<float, false>(p, z, st);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? FRNNT_OK : FRNNT_ERR_CUDA;
 }
@@ -184,15 +597,10 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs_bwd", st);
-    if (d->dtype == FRNNT_BF16)
-      logprob_bwd_kernel<__nv_bfloat16><<<d->N, kThreads, 0, st>>>(
-          d->V, d->K, d->top, d->ld, d->ldd, (const __nv_bfloat16*)logits, tokens, lse, entropy, top_ids, dlogp,
-          dentropy, dtop, (__nv_bfloat16*)dlogits, status);
-    else
-      logprob_bwd_kernel<float><<<d->N, kThreads, 0, st>>>(d->V, d->K, d->top, d->ld, d->ldd, (const float*)logits,
-                                                           tokens, lse, entropy, top_ids, dlogp, dentropy, dtop,
-                                                           (float*)dlogits, status);
-    note_launch();
+    const BwdParams p{d->N, d->V, d->K, d->top, 1, d->ld, d->ldd, tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,
+                      status};
+    if (d->dtype == FRNNT_BF16) launch_bwd(p, (const __nv_bfloat16*)logits, (__nv_bfloat16*)dlogits, st);
+    else launch_bwd(p, (const float*)logits, (float*)dlogits, st);
   }
   return cudaGetLastError() == cudaSuccess ? FRNNT_OK : FRNNT_ERR_CUDA;
 }

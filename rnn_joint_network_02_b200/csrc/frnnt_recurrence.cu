@@ -83,13 +83,10 @@ __device__ __forceinline__ void store_pair(T* p, float a, float b, bool two) {
   }
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// Writes v to the same shared-memory place of CTA `rank` of the cluster.
+// Writes v to the same shared-memory place of block `rank` of the cluster.
 __device__ __forceinline__ void store_cluster(float4* p, float4 v, int rank) {
-  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(r), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(in_cluster(p, rank)), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
                : "memory");
 }
 
