@@ -15,33 +15,6 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // would be NaN.
 constexpr float kFloor = -160.f;
 
-// ------------------------------------------------------------------ arithmetic on pairs
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 open(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -201,21 +174,21 @@ __device__ __forceinline__ void scan_row(const Row<T>& row, int g, int G, int la
     if (ref > st.m) rescale(st, ref);
     // a lane that has seen only -inf (or NaN) sums about 0
     const float at = ref == -INFINITY ? 0.f : -ref;
-    const uint64_t at2 = pair(at, at), l2e = pair(kLog2e, kLog2e);
-    uint64_t s2 = pair(0.f, 0.f), w2 = s2;
+    const uint64_t at2 = f2_of(at, at), l2e = f2_of(kLog2e, kLog2e);
+    uint64_t s2 = f2_of(0.f, 0.f), w2 = s2;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
       if (u < n) {
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
-          const float2 d = open(mul2(add2(pair(z[u][i], z[u][i + 1]), at2), l2e));
+          const float2 d = f2_open(f2_mul(f2_add(f2_of(z[u][i], z[u][i + 1]), at2), l2e));
           const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
-          const uint64_t e2 = pair(exp2_approx(d0), exp2_approx(d1));
-          s2 = add2(s2, e2);
-          w2 = fma2(e2, pair(d0, d1), w2);
+          const uint64_t e2 = f2_of(exp2_approx(d0), exp2_approx(d1));
+          s2 = f2_add(s2, e2);
+          w2 = f2_fma(e2, f2_of(d0, d1), w2);
         }
       }
-    const float2 s = open(s2), w = open(w2);
+    const float2 s = f2_open(s2), w = f2_open(w2);
     st.s += s.x + s.y;
     st.w += w.x + w.y;
 
@@ -473,7 +446,7 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   };
 
   const bool whole = ((uintptr_t)(out + row.head) & 15u) == 0;
-  const uint64_t l2 = pair(-l, -l), l2e = pair(kLog2e, kLog2e), A2 = pair(A, A), B2 = pair(B, B);
+  const uint64_t l2 = f2_of(-l, -l), l2e = f2_of(kLog2e, kLog2e), A2 = f2_of(A, A), B2 = f2_of(B, B);
   for (int base = v0; base < v1; base += 32 * kVecs) {
     uint4 raw[kVecs];
 #pragma unroll
@@ -489,9 +462,9 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
         unpack<T>(raw[u], f);
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
-          const float2 d = open(mul2(add2(pair(f[i], f[i + 1]), l2), l2e));
+          const float2 d = f2_open(f2_mul(f2_add(f2_of(f[i], f[i + 1]), l2), l2e));
           const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
-          const float2 g = open(mul2(pair(-exp2_approx(d0), -exp2_approx(d1)), fma2(B2, pair(d0, d1), A2)));
+          const float2 g = f2_open(f2_mul(f2_of(-exp2_approx(d0), -exp2_approx(d1)), f2_fma(B2, f2_of(d0, d1), A2)));
           f[i] = none ? 0.f : g.x;
           f[i + 1] = none ? 0.f : g.y;
         }

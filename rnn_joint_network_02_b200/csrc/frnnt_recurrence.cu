@@ -1,35 +1,50 @@
 // Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t, a = sigmoid(gate):
 // forward over padded sequences, backward, and one step of many hypotheses.
+#include <atomic>
 #include <initializer_list>
 
 #include "frnnt_common.cuh"
 #include "frnnt_internal.h"
 #include "frnnt_ops.h"
+#include "sm100.cuh"
 
 namespace frnnt {
 namespace {
 
-// A block walks along one sequence, 64 channels wide, kChunk steps at a time.
-// Lane l of every warp holds channels 2l and 2l+1 (one 4- or 8-byte access a
-// step, 32 lanes side by side); warp w takes the kSteps steps from w * kSteps on.
+// A block walks along one sequence, kTile channels wide, kChunk steps at a
+// time.  Lane l of every warp holds channels 2l and 2l + 1; warp w takes the
+// kSteps steps from w * kSteps on.
 constexpr int kChunk = FRNNT_SCAN_CHUNK;
-constexpr int kSteps = 8;
+constexpr int kSteps = 16;
 constexpr int kWarps = kChunk / kSteps;
 constexpr int kTile = 64;
+static_assert(kWarps >= 8, "a warp for each block of a cluster");
+// Blocks an SM is to hold: shared memory and registers are dealt out for that.
+template <typename T>
+constexpr int blocks_of() {
+  return sizeof(T) == 2 ? 2 : 1;
+}
 
 // a = sigmoid(gate) and s = 1 - a = sigmoid(-gate), each to relative precision:
 // with e = exp(-gate), a = 1 / (1 + e), and s = e a where that is below 1/2 (1 -
 // a would lose its digits where the memory is long and a is near 1), 1 - a
 // above (where e may be infinite).  The hardware exp2 and reciprocal are good
 // to 2^-22, and the rounded exponent adds |gate| 2^-24.
-struct Gate {
-  float a, s;
+struct Gates {   // of two channels
+  uint64_t a, s;
 };
-__device__ __forceinline__ Gate gate_of(float g) {
-  float e, a;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
-  return Gate{a, e > 1.f ? 1.f - a : e * a};
+__device__ __forceinline__ Gates gates_of(uint64_t g) {
+  const float2 x = f2_open(f2_mul(g, f2_of(-1.44269504f, -1.44269504f)));
+  float e0, e1, a0, a1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x.y));
+  const uint64_t e = f2_of(e0, e1), one = f2_of(1.f, 1.f);
+  const float2 d = f2_open(f2_add(e, one));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(d.y));
+  const uint64_t a = f2_of(a0, a1);
+  const float2 small = f2_open(f2_mul(e, a)), big = f2_open(f2_fma(a, f2_of(-1.f, -1.f), one));
+  return Gates{a, f2_of(e0 > 1.f ? big.x : small.x, e1 > 1.f ? big.y : small.y)};
 }
 
 __device__ __forceinline__ int length_of(const int32_t* lengths, int b, int T, int32_t* status) {
@@ -45,288 +60,355 @@ struct Pair;
 template <>
 struct Pair<float> {
   using Raw = float2;
-  static __device__ __forceinline__ float2 open(float2 r) { return r; }
-  static __device__ __forceinline__ float2 pack(float a, float b) { return make_float2(a, b); }
-  static __device__ __forceinline__ float2 join(float a, float b) { return make_float2(a, b); }
+  static __device__ __forceinline__ uint64_t open(float2 r) { return f2_of(r.x, r.y); }
+  static __device__ __forceinline__ float2 pack(float2 v) { return v; }
 };
 template <>
 struct Pair<__nv_bfloat16> {
   using Raw = uint32_t;
-  static __device__ __forceinline__ float2 open(uint32_t r) {
-    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
+  static __device__ __forceinline__ uint64_t open(uint32_t r) {
+    return f2_of(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  static __device__ __forceinline__ uint32_t pack(float2 f) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  static __device__ __forceinline__ uint32_t join(__nv_bfloat16 a, __nv_bfloat16 b) {
-    return (uint32_t)__bfloat16_as_ushort(a) | ((uint32_t)__bfloat16_as_ushort(b) << 16);
   }
 };
 
-// VEC: every pair is aligned to its size and D is even; otherwise channel by
-// channel, `two` telling whether the second exists.
+// One array of a chunk in shared memory: kChunk steps of kTile channels.
+template <typename T>
+struct Stage {
+  T v[kChunk][kTile];
+  __device__ __forceinline__ uint64_t at(int t, int lane) const {
+    return Pair<T>::open(reinterpret_cast<const typename Pair<T>::Raw*>(v[t])[lane]);
+  }
+};
+
+// Copies rows t0 .. t0 + 16 warps - 1 (those in [0, len)) of channels c0 ..
+// into `to`.  VEC: the rows start on 16-byte boundaries and are copied
+// asynchronously, 16 bytes a thread; otherwise element by element.
 template <typename T, bool VEC>
-__device__ __forceinline__ typename Pair<T>::Raw load_pair(const T* p, bool two) {
-  using Raw = typename Pair<T>::Raw;
-  if (VEC) return __ldg(reinterpret_cast<const Raw*>(p));
-  return Pair<T>::join(__ldg(p), two ? __ldg(p + 1) : from_f32<T>(0.f));
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_pair(T* p, float a, float b, bool two) {
-  using Raw = typename Pair<T>::Raw;
+__device__ __forceinline__ void load_stage(Stage<T>& to, const T* __restrict__ p, long long step, int t0, int len,
+                                           int c0, int D) {
   if (VEC) {
-    *reinterpret_cast<Raw*>(p) = Pair<T>::pack(a, b);
+    constexpr int E = 16 / sizeof(T), kPerRow = kTile / E;
+    const int j = threadIdx.x % kPerRow, c = c0 + j * E;
+    const int rows = blockDim.x / kPerRow, bytes = min(E, D - c) * (int)sizeof(T);
+    if (c >= D) return;
+    const int first = threadIdx.x / kPerRow;
+    const T* src = p + (t0 + first) * step + c;
+    uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&to.v[first][j * E]));
+#pragma unroll
+    for (int k = 0; k < kSteps * kPerRow / 32; ++k) {
+      if (t0 + first + k * rows < len)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+      src += rows * step;
+      dst += rows * kTile * sizeof(T);
+    }
   } else {
-    p[0] = from_f32<T>(a);
-    if (two) p[1] = from_f32<T>(b);
+    for (int i = threadIdx.x; i < (int)(blockDim.x / 32) * kSteps * kTile; i += blockDim.x) {
+      const int t = i / kTile, c = i % kTile;
+      if (t0 + t < len && c0 + c < D) to.v[t][c] = p[(t0 + t) * step + c0 + c];
+    }
   }
 }
 
-// Writes v to the same shared-memory place of block `rank` of the cluster.
-__device__ __forceinline__ void store_cluster(float4* p, float4 v, int rank) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(in_cluster(p, rank)), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_pair(T* p, float2 v, bool two) {
+  using Raw = typename Pair<T>::Raw;
+  if (VEC) {
+    *reinterpret_cast<Raw*>(p) = Pair<T>::pack(v);
+  } else {
+    p[0] = from_f32<T>(v.x);
+    if (two) p[1] = from_f32<T>(v.y);
+  }
 }
 
+// Per-sequence channels c and c + 1 of a [rows, D] fp32 array.
+__device__ __forceinline__ uint64_t load_state(const float* p, long long row, int D, int c, bool live, bool two) {
+  if (!p || !live) return f2_of(0.f, 0.f);
+  const float* q = p + row * D + c;
+  return f2_of(q[0], two ? q[1] : 0.f);
+}
+__device__ __forceinline__ void store_state(float* p, long long row, int D, int c, bool live, bool two, uint64_t v) {
+  if (!p || !live) return;
+  const float2 f = f2_open(v);
+  p[row * D + c] = f.x;
+  if (two) p[row * D + c + 1] = f.y;
+}
+
+// A run of steps as a map of its entering value: out = A in + R.
+struct Map {
+  uint64_t A, R;
+};
+__device__ __forceinline__ Map map_one() { return Map{f2_of(1.f, 1.f), f2_of(0.f, 0.f)}; }
+__device__ __forceinline__ Map then(Map f, Map g) { return Map{f2_mul(g.A, f.A), f2_fma(g.A, f.R, g.R)}; }
+__device__ __forceinline__ uint64_t apply(Map f, uint64_t v) { return f2_fma(f.A, v, f.R); }
+
+// The blocks of a cluster tell each other the map of their chunk: every block
+// sends it to every block's shared memory, where an mbarrier counts the bytes of
+// all CL maps.  Two buffers: a block that sends round r + 2 has received
+// round r + 1 from all, and each sent that after all its threads had read round r.
+template <int CL>
+struct Exchange {
+  ulonglong2 maps[2][CL][32];
+  uint64_t full[2];
+
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      sm100::mbar_init(&full[0], 1);
+      sm100::mbar_init(&full[1], 1);
+      sm100::fence_barrier_init();
+    }
+  }
+  __device__ __forceinline__ void send(int r, int rank, int lane, int w, Map m) {
+    if (threadIdx.x == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * 32 * sizeof(ulonglong2));
+    if (w < CL)
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+                       in_cluster(&maps[r & 1][rank][lane], w)),
+                   "l"(m.A), "l"(m.R), "r"(in_cluster(&full[r & 1], w))
+                   : "memory");
+  }
+  // The carry after this round; `in`: what enters block `rank`'s chunk.
+  __device__ __forceinline__ uint64_t receive(int r, int rank, int lane, uint64_t carry, uint64_t& in, int32_t* status) {
+    bool ok = sm100::mbar_try_wait_cluster(&full[r & 1], (r >> 1) & 1, 0);
+    for (uint32_t i = 0; !ok && i < sm100::kMaxTries; ++i)
+      ok = sm100::mbar_try_wait_cluster(&full[r & 1], (r >> 1) & 1, sm100::kSuspendNs);
+    if (!ok && status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
+    for (int k = 0; k < CL; ++k) {
+      if (k == rank) in = carry;
+      const ulonglong2 o = maps[r & 1][k][lane];
+      carry = f2_fma(o.x, carry, o.y);
+    }
+    return carry;
+  }
+};
+template <>
+struct Exchange<1> {
+  __device__ __forceinline__ void init() {}
+};
+
 // Forward.  h_t = a_t h_{t-1} + b_t composes: over a run of steps h_out = A h_in
-// + H with A the product of the a and H the run's result from zero.  Each
-// warp forms its run's (A, H), the block joins them in shared memory, and
-// each warp walks its run again from its true entering state, out of
-// registers: x and gate are read once, h written once.  The block carries the
-// state from chunk to chunk.  Where there are too few (sequence, channel
-// tile) pairs to fill the GPU, CL blocks of a cluster take the chunks in turn
-// and tell each other their chunk's (A, H) through distributed shared memory,
-// one cluster barrier a round.
-template <typename T, bool VEC, int CL>
-__global__ void __launch_bounds__(kWarps * 32)
+// + R with A the product of the a and R the run's result from zero.  Each
+// warp forms its run's map, the block joins them in shared memory, and each
+// warp walks its run again from its true entering state, out of registers: x
+// and gate are read once, h written once.  The block carries the state from
+// chunk to chunk and has the next chunks on their way meanwhile.  Where there
+// are too few (sequence, channel tile) pairs to fill the GPU, CL blocks of a
+// cluster take the chunks in turn.
+template <typename T, bool VEC, int CL, int STAGES>
+__global__ void __launch_bounds__(kWarps * 32, blocks_of<T>())
     scan_fwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ h0, T* __restrict__ h,
                     float* __restrict__ h_last, float* __restrict__ saved, int32_t* status) {
-  using Raw = typename Pair<T>::Raw;
-  __shared__ float4 run[2][kWarps][32];
-  __shared__ float4 part[2][CL][32];
+  extern __shared__ __align__(128) unsigned char smem[];
+  Stage<T>* stage = reinterpret_cast<Stage<T>*>(smem);   // [STAGES][x, gate]
+  __shared__ ulonglong2 run[kWarps][32];
+  __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c = (blockIdx.x / CL) * kTile + 2 * lane;
+  const int c0 = (blockIdx.x / CL) * kTile, c = c0 + 2 * lane;
   const bool live = c < d.D, two = c + 1 < d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
-  const T* xp = x + b * d.x_sb + c;
-  const T* gp = gate + b * d.gate_sb + c;
+  const T* xp = x + b * d.x_sb;
+  const T* gp = gate + b * d.gate_sb;
   T* hp = h + b * d.h_sb + c;
+  ex.init();
   if (CL > 1) cluster_arrive();
-
-  Raw rx[kSteps], rg[kSteps];
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-      if (live && t0 + i < len) {
-        rx[i] = load_pair<T, VEC>(xp + (t0 + i) * d.x_st, two);
-        rg[i] = load_pair<T, VEC>(gp + (t0 + i) * d.gate_st, two);
-      }
+  auto fetch = [&](int r) {
+    if (r < rounds) {
+      const int t = (r * CL + rank) * kChunk;
+      load_stage<T, VEC>(stage[2 * (r % STAGES)], xp, d.x_st, t, len, c0, d.D);
+      load_stage<T, VEC>(stage[2 * (r % STAGES) + 1], gp, d.gate_st, t, len, c0, d.D);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float2 carry = make_float2(0.f, 0.f);
-  if (h0 && live) carry = make_float2(h0[(long long)b * d.D + c], two ? h0[(long long)b * d.D + c + 1] : 0.f);
-  int t0 = rank * kChunk + w * kSteps;
-  if (rounds > 0) fetch(t0);
-  if (CL > 1) cluster_wait();     // the other blocks run: their shared memory may be written from here on
-  for (int r = 0; r < rounds; ++r, t0 += CL * kChunk) {
-    float2 a[kSteps], v[kSteps];
-    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);   // A, H of the two channels
+#pragma unroll
+  for (int r = 0; r < STAGES - 1; ++r) fetch(r);
+  uint64_t carry = load_state(h0, b, d.D, c, live, two);
+  if (CL > 1) cluster_wait();     // the other blocks run, their mbarriers are ready
+  for (int r = 0; r < rounds; ++r) {
+    const int t0 = (r * CL + rank) * kChunk + w * kSteps;
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncthreads();              // this round's rows are here; the stage before is free
+    fetch(r + STAGES - 1);
+    const Stage<T>&sx = stage[2 * (r % STAGES)], &sg = stage[2 * (r % STAGES) + 1];
+    uint64_t a[kSteps], v[kSteps];
+    Map m = map_one();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      a[i] = make_float2(1.f, 1.f);
-      v[i] = make_float2(0.f, 0.f);
-      if (live && t0 + i < len) {
-        const float2 xv = Pair<T>::open(rx[i]), gv = Pair<T>::open(rg[i]);
-        const Gate g0 = gate_of(gv.x), g1 = gate_of(gv.y);
-        a[i] = make_float2(g0.a, g1.a);
-        v[i] = make_float2(g0.s * xv.x, g1.s * xv.y);
-      }
-      m.x *= a[i].x;
-      m.y = fmaf(a[i].x, m.y, v[i].x);
-      m.z *= a[i].y;
-      m.w = fmaf(a[i].y, m.w, v[i].y);
+      const Gates g = gates_of(sg.at(w * kSteps + i, lane));
+      a[i] = g.a;
+      v[i] = f2_mul(g.s, sx.at(w * kSteps + i, lane));
     }
-    if (r + 1 < rounds) fetch(t0 + CL * kChunk);
-    run[r & 1][w][lane] = m;
-    __syncthreads();
-    float4 before = make_float4(1.f, 0.f, 1.f, 0.f), all = before;   // runs before this warp's; the whole chunk
-    for (int k = 0; k < nw; ++k) {
-      if (k == w) before = all;
-      const float4 o = run[r & 1][k][lane];
-      all = make_float4(all.x * o.x, fmaf(o.x, all.y, o.y), all.z * o.z, fmaf(o.z, all.w, o.w));
-    }
-    float2 in = carry;              // the state that enters this block's chunk
-    if (CL > 1) {
-      if (w < CL) store_cluster(&part[r & 1][rank][lane], all, w);
-      cluster_arrive();
-      cluster_wait();
+    const bool whole = t0 + kSteps <= len;
+    if (!whole) {                 // steps past the sequence leave the state as it is
 #pragma unroll
-      for (int k = 0; k < CL; ++k) {
-        if (k == rank) in = carry;
-        const float4 o = part[r & 1][k][lane];
-        carry = make_float2(fmaf(o.x, carry.x, o.y), fmaf(o.z, carry.y, o.w));
+      for (int i = 0; i < kSteps; ++i)
+        if (t0 + i >= len) {
+          a[i] = f2_of(1.f, 1.f);
+          v[i] = f2_of(0.f, 0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) m = then(m, Map{a[i], v[i]});
+    run[w][lane] = make_ulonglong2(m.A, m.R);
+    __syncthreads();
+    Map before = map_one();       // the runs before this warp's
+    for (int k = 0; k < w; ++k) {
+      const ulonglong2 o = run[k][lane];
+      before = then(before, Map{o.x, o.y});
+    }
+    Map all = then(before, m);    // the chunk
+    for (int k = w + 1; k < nw; ++k) {
+      const ulonglong2 o = run[k][lane];
+      all = then(all, Map{o.x, o.y});
+    }
+    uint64_t in = carry;
+    if constexpr (CL > 1) {
+      ex.send(r, rank, lane, w, all);
+      carry = ex.receive(r, rank, lane, carry, in, status);
+    } else {
+      carry = apply(all, carry);
+    }
+    if (w == 0 && t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
+    uint64_t s = apply(before, in);
+    T* q = hp + t0 * d.h_st;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i, q += d.h_st) {
+        s = f2_fma(a[i], s, v[i]);
+        if (live) store_pair<T, VEC>(q, f2_open(s), two);
       }
     } else {
-      carry = make_float2(fmaf(all.x, carry.x, all.y), fmaf(all.z, carry.y, all.w));
-    }
-    if (saved && w == 0 && live && t0 < len) {
-      float* sp = saved + ((long long)b * nc + t0 / kChunk) * d.D + c;
-      sp[0] = in.x;
-      if (two) sp[1] = in.y;
-    }
-    float2 s = make_float2(fmaf(before.x, in.x, before.y), fmaf(before.z, in.y, before.w));
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      s = make_float2(fmaf(a[i].x, s.x, v[i].x), fmaf(a[i].y, s.y, v[i].y));
-      if (live && t0 + i < d.T) {
-        const bool on = t0 + i < len;
-        store_pair<T, VEC>(hp + (t0 + i) * d.h_st, on ? s.x : 0.f, on ? s.y : 0.f, two);
+      for (int i = 0; i < kSteps; ++i, q += d.h_st) {
+        s = f2_fma(a[i], s, v[i]);
+        if (live && t0 + i < d.T) store_pair<T, VEC>(q, t0 + i < len ? f2_open(s) : make_float2(0.f, 0.f), two);
       }
     }
   }
   // rows of whole rounds past the sequence
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
-    if (live) store_pair<T, VEC>(hp + t * d.h_st, 0.f, 0.f, two);
-  if (rank == 0 && w == 0 && live) {
-    h_last[(long long)b * d.D + c] = carry.x;
-    if (two) h_last[(long long)b * d.D + c + 1] = carry.y;
-  }
+    if (live) store_pair<T, VEC>(hp + t * d.h_st, make_float2(0.f, 0.f), two);
+  if (rank == 0 && w == 0) store_state(h_last, b, d.D, c, live, two, carry);
 }
 
-// Backward.  With q_t = a_t g_t, what step t hands to step t-1, q_t = a_t
+// Backward.  With q_t = a_t g_t, what step t hands to step t - 1, q_t = a_t
 // (q_{t+1} + dh_t) is the same recurrence run from the end: over a run of
 // steps q_out = A q_in + Q with the same A.  The chunk's states are formed
-// again from its saved state by the forward composition, in the same exchange,
-// so x, gate and dh are read once, dx and dgate written once, and h is not read.
-template <typename T, bool VEC, int CL>
-__global__ void __launch_bounds__(kWarps * 32)
+// again from its saved state by the forward maps, in the same exchange, so x,
+// gate and dh are read once, dx and dgate written once, and h is not read.
+template <typename T, bool VEC, int CL, int STAGES>
+__global__ void __launch_bounds__(kWarps * 32, blocks_of<T>())
     scan_bwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ saved, const T* __restrict__ dh,
                     const float* __restrict__ dh_last, T* __restrict__ dx, T* __restrict__ dgate,
                     float* __restrict__ dh0, int32_t* status) {
-  using Raw = typename Pair<T>::Raw;
-  __shared__ float4 run[2][kWarps][32];    // A, H of the two channels
-  __shared__ float2 back[2][kWarps][32];   // Q
-  __shared__ float4 part[2][CL][32];       // A, Q of a block's chunk
+  extern __shared__ __align__(128) unsigned char smem[];
+  Stage<T>* stage = reinterpret_cast<Stage<T>*>(smem);   // [STAGES][x, gate, dh]
+  __shared__ ulonglong2 run[kWarps][32];   // forward maps
+  __shared__ uint64_t back[kWarps][32];    // Q of the backward maps
+  __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c = (blockIdx.x / CL) * kTile + 2 * lane;
+  const int c0 = (blockIdx.x / CL) * kTile, c = c0 + 2 * lane;
   const bool live = c < d.D, two = c + 1 < d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
-  const T* xp = x + b * d.x_sb + c;
-  const T* gp = gate + b * d.gate_sb + c;
-  const T* hp = dh + b * d.dh_sb + c;
+  const T* xp = x + b * d.x_sb;
+  const T* gp = gate + b * d.gate_sb;
+  const T* hp = dh + b * d.dh_sb;
   T* dxp = dx + b * d.dx_sb + c;
   T* dgp = dgate + b * d.dgate_sb + c;
+  ex.init();
   if (CL > 1) cluster_arrive();
-
-  Raw rx[kSteps], rg[kSteps], rh[kSteps];
-  float2 start = make_float2(0.f, 0.f);
-  auto fetch = [&](int t0) {
+  // rounds from the end; within a round rank 0 has the latest chunk
+  auto chunk_at = [&](int r) { return ((rounds - r) * CL - 1 - rank) * kChunk; };
+  auto fetch = [&](int r) {
+    if (r < rounds) {
+      const int t = chunk_at(r);
+      Stage<T>* to = stage + 3 * (r % STAGES);
+      load_stage<T, VEC>(to[0], xp, d.x_st, t, len, c0, d.D);
+      load_stage<T, VEC>(to[1], gp, d.gate_st, t, len, c0, d.D);
+      load_stage<T, VEC>(to[2], hp, d.dh_st, t, len, c0, d.D);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int r = 0; r < STAGES - 1; ++r) fetch(r);
+  uint64_t carry = load_state(dh_last, b, d.D, c, live, two);
+  if (CL > 1) cluster_wait();
+  for (int r = 0; r < rounds; ++r) {
+    const int t0 = chunk_at(r) + w * kSteps;
+    uint64_t v = load_state(t0 < len ? saved : nullptr, (long long)b * nc + t0 / kChunk, d.D, c, live, two);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncthreads();              // this round's rows are here; the stage before is free
+    fetch(r + STAGES - 1);
+    const Stage<T>* at = stage + 3 * (r % STAGES);
+    uint64_t a[kSteps], s[kSteps], past[kSteps];
+    Map m = map_one();
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const Gates g = gates_of(at[1].at(w * kSteps + i, lane));
+      a[i] = g.a;
+      s[i] = g.s;
+    }
+    const bool whole = t0 + kSteps <= len;
+    const int n = whole ? kSteps : max(0, len - t0);   // steps within the sequence
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      if (live && t0 + i < len && t0 >= 0) {
-        rx[i] = load_pair<T, VEC>(xp + (t0 + i) * d.x_st, two);
-        rg[i] = load_pair<T, VEC>(gp + (t0 + i) * d.gate_st, two);
-        rh[i] = load_pair<T, VEC>(hp + (t0 + i) * d.dh_st, two);
-      }
-    if (live && t0 >= 0 && t0 < len) {
-      const float* sp = saved + ((long long)b * nc + t0 / kChunk) * d.D + c;
-      start = make_float2(sp[0], two ? sp[1] : 0.f);
-    }
-  };
-  float2 carry = make_float2(0.f, 0.f);
-  if (dh_last && live)
-    carry = make_float2(dh_last[(long long)b * d.D + c], two ? dh_last[(long long)b * d.D + c + 1] : 0.f);
-  // rounds from the end; within a round rank 0 has the latest chunk
-  int t0 = (rounds * CL - 1 - rank) * kChunk + w * kSteps;
-  if (rounds > 0) fetch(t0);
-  if (CL > 1) cluster_wait();
-  for (int r = 0; r < rounds; ++r, t0 -= CL * kChunk) {
-    float2 a[kSteps], s[kSteps], xv[kSteps], e[kSteps], past[kSteps];
-    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (whole || i < n) m = then(m, Map{a[i], f2_mul(s[i], at[0].at(w * kSteps + i, lane))});
+    uint64_t q = f2_of(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      a[i] = make_float2(1.f, 1.f);
-      s[i] = xv[i] = e[i] = make_float2(0.f, 0.f);
-      if (live && t0 + i < len) {
-        const float2 gv = Pair<T>::open(rg[i]);
-        const Gate g0 = gate_of(gv.x), g1 = gate_of(gv.y);
-        a[i] = make_float2(g0.a, g1.a);
-        s[i] = make_float2(g0.s, g1.s);
-        xv[i] = Pair<T>::open(rx[i]);
-        e[i] = Pair<T>::open(rh[i]);
-      }
-      m.x *= a[i].x;
-      m.y = fmaf(a[i].x, m.y, s[i].x * xv[i].x);
-      m.z *= a[i].y;
-      m.w = fmaf(a[i].y, m.w, s[i].y * xv[i].y);
-    }
-    float2 q = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i) q = make_float2(a[i].x * (q.x + e[i].x), a[i].y * (q.y + e[i].y));
-    float2 v = start;
-    if (r + 1 < rounds) fetch(t0 - CL * kChunk);
-    run[r & 1][w][lane] = m;
-    back[r & 1][w][lane] = q;
+    for (int i = kSteps - 1; i >= 0; --i)
+      if (whole || i < n) q = f2_mul(a[i], f2_add(q, at[2].at(w * kSteps + i, lane)));
+    run[w][lane] = make_ulonglong2(m.A, m.R);
+    back[w][lane] = q;
     __syncthreads();
     for (int k = 0; k < w; ++k) {
-      const float4 o = run[r & 1][k][lane];
-      v = make_float2(fmaf(o.x, v.x, o.y), fmaf(o.z, v.y, o.w));
+      const ulonglong2 o = run[k][lane];
+      v = f2_fma(o.x, v, o.y);
     }
-    float4 before = make_float4(1.f, 0.f, 1.f, 0.f), all = before;   // runs after this warp's; the whole chunk
-    for (int k = nw - 1; k >= 0; --k) {
-      if (k == w) before = all;
-      const float4 o = run[r & 1][k][lane];
-      const float2 p = back[r & 1][k][lane];
-      all = make_float4(all.x * o.x, fmaf(o.x, all.y, p.x), all.z * o.z, fmaf(o.z, all.w, p.y));
-    }
-    float2 in = carry;
-    if (CL > 1) {
-      if (w < CL) store_cluster(&part[r & 1][rank][lane], all, w);
-      cluster_arrive();
-      cluster_wait();
+    Map after = map_one();        // the runs after this warp's, from the end
+    for (int k = nw - 1; k > w; --k) after = then(after, Map{run[k][lane].x, back[k][lane]});
+    Map all = then(after, Map{m.A, q});
+    for (int k = w - 1; k >= 0; --k) all = then(all, Map{run[k][lane].x, back[k][lane]});
+    uint64_t in = carry;
+    if constexpr (CL > 1) ex.send(r, rank, lane, w, all);
 #pragma unroll
-      for (int k = 0; k < CL; ++k) {
-        if (k == rank) in = carry;
-        const float4 o = part[r & 1][k][lane];
-        carry = make_float2(fmaf(o.x, carry.x, o.y), fmaf(o.z, carry.y, o.w));
-      }
-    } else {
-      carry = make_float2(fmaf(all.x, carry.x, all.y), fmaf(all.z, carry.y, all.w));
+    for (int i = 0; i < kSteps; ++i) {   // the states again, while the maps travel
+      const uint64_t xv = at[0].at(w * kSteps + i, lane);
+      past[i] = f2_fma(xv, f2_of(-1.f, -1.f), v);
+      v = f2_fma(a[i], v, f2_mul(s[i], xv));
     }
+    if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, status);
+    else carry = apply(all, carry);
+    q = apply(after, in);
+    T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
+    T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      past[i] = make_float2(v.x - xv[i].x, v.y - xv[i].y);
-      v = make_float2(fmaf(a[i].x, v.x, s[i].x * xv[i].x), fmaf(a[i].y, v.y, s[i].y * xv[i].y));
-    }
-    q = make_float2(fmaf(before.x, in.x, before.y), fmaf(before.z, in.y, before.w));
-#pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i) {
-      const float2 g = make_float2(q.x + e[i].x, q.y + e[i].y);
-      q = make_float2(a[i].x * g.x, a[i].y * g.y);
-      if (live && t0 + i < d.T && t0 >= 0) {
-        const bool on = t0 + i < len;
-        store_pair<T, VEC>(dxp + (t0 + i) * d.dx_st, on ? s[i].x * g.x : 0.f, on ? s[i].y * g.y : 0.f, two);
-        store_pair<T, VEC>(dgp + (t0 + i) * d.dgate_st, on ? q.x * s[i].x * past[i].x : 0.f,
-                           on ? q.y * s[i].y * past[i].y : 0.f, two);
+    for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
+      if (whole || i < n) {
+        const uint64_t g = f2_add(q, at[2].at(w * kSteps + i, lane));
+        q = f2_mul(a[i], g);
+        if (live) {
+          store_pair<T, VEC>(px, f2_open(f2_mul(s[i], g)), two);
+          store_pair<T, VEC>(pg, f2_open(f2_mul(f2_mul(q, s[i]), past[i])), two);
+        }
+      } else if (live && t0 + i < d.T) {
+        store_pair<T, VEC>(px, make_float2(0.f, 0.f), two);
+        store_pair<T, VEC>(pg, make_float2(0.f, 0.f), two);
       }
     }
   }
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
     if (live) {
-      store_pair<T, VEC>(dxp + t * d.dx_st, 0.f, 0.f, two);
-      store_pair<T, VEC>(dgp + t * d.dgate_st, 0.f, 0.f, two);
+      store_pair<T, VEC>(dxp + t * d.dx_st, make_float2(0.f, 0.f), two);
+      store_pair<T, VEC>(dgp + t * d.dgate_st, make_float2(0.f, 0.f), two);
     }
-  if (dh0 && rank == 0 && w == 0 && live) {
-    dh0[(long long)b * d.D + c] = carry.x;
-    if (two) dh0[(long long)b * d.D + c + 1] = carry.y;
-  }
+  if (rank == 0 && w == 0) store_state(dh0, b, d.D, c, live, two, carry);
 }
 
 template <typename T>
@@ -343,8 +425,8 @@ __global__ void step_kernel(frnnt_step_dims d, const T* x, const T* gate, const 
   }
   float v = state[(long long)from * d.D + c];
   if (!advance || advance[n]) {
-    const Gate g = gate_of(to_f32<T>(gate[n * d.gate_sn + c]));
-    v = fmaf(g.a, v, g.s * to_f32<T>(x[n * d.x_sn + c]));
+    const Gates g = gates_of(f2_of(to_f32<T>(gate[n * d.gate_sn + c]), 0.f));
+    v = fmaf(f2_open(g.a).x, v, f2_open(g.s).x * to_f32<T>(x[n * d.x_sn + c]));
   }
   new_state[n * d.D + c] = v;
   h[n * d.D + c] = from_f32<T>(v);
@@ -388,53 +470,76 @@ int cluster_of(const frnnt_recurrence_dims& d) {
   return cl;
 }
 
-template <typename... P, typename... A>
-void launch_scan(void (*kernel)(P...), const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
+// Chunks in shared memory at a time: what leaves room for blocks_of<T>() blocks
+// on an SM (three of two arrays, two of three).
+constexpr int stages_of(int arrays) { return arrays == 2 ? 3 : 2; }
+
+template <typename T, int ARRAYS, auto kernel, typename... A>
+int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
+  constexpr int bytes = (int)sizeof(Stage<T>) * ARRAYS * stages_of(ARRAYS);
+  static std::atomic<bool> ready[kDeviceSlots];
+  std::atomic<bool>& here = ready[current_device()];
+  if (!here.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return FRNNT_ERR_CUDA;
+    here.store(true, std::memory_order_release);
+  }
   const int warps = d.T < kChunk ? (d.T + kSteps - 1) / kSteps : kWarps;
   const dim3 grid((d.D + kTile - 1) / kTile * cl, d.B);
-  launch_k(kernel, grid, dim3(warps * 32), 0, st, cl, args...);
+  launch_k(kernel, grid, dim3(warps * 32), bytes, st, cl, args...);
   note_launch();
+  return FRNNT_OK;
 }
 
-// Pairs of channels can be moved whole.
-bool pairs_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void*> ptrs,
-              std::initializer_list<long long> strides) {
+// Rows of 16-byte vectors throughout.
+bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void*> ptrs,
+                std::initializer_list<long long> strides) {
   if (d.D % 2) return false;
   for (const void* p : ptrs)
-    if (!aligned(p, 2 * size_of(d.dtype))) return false;
+    if (!aligned(p, 16)) return false;
   for (long long v : strides)
-    if (v % 2) return false;
+    if (v * size_of(d.dtype) % 16) return false;
   return true;
 }
 
-template <typename T, bool VEC>
-void scan_fwd(const frnnt_recurrence_dims& d, const void* x, const void* gate, const int32_t* lengths,
-              const float* h0, void* h, float* h_last, float* saved, int32_t* status, cudaStream_t st) {
-  auto go = [&](auto kernel, int cl) {
-    launch_scan(kernel, d, cl, st, d, (const T*)x, (const T*)gate, lengths, h0, (T*)h, h_last, saved, status);
-  };
+template <typename T, bool VEC, typename... A>
+int scan_fwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
+  constexpr int S = stages_of(2);
   switch (cluster_of(d)) {
-    case 1: return go(scan_fwd_kernel<T, VEC, 1>, 1);
-    case 2: return go(scan_fwd_kernel<T, VEC, 2>, 2);
-    case 4: return go(scan_fwd_kernel<T, VEC, 4>, 4);
-    default: return go(scan_fwd_kernel<T, VEC, 8>, 8);
+    case 1: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
+    case 2: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
+    case 4: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
+    default: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
   }
 }
 
-template <typename T, bool VEC>
-void scan_bwd(const frnnt_recurrence_dims& d, const void* x, const void* gate, const int32_t* lengths,
-              const float* saved, const void* dh, const float* dh_last, void* dx, void* dgate, float* dh0,
-              int32_t* status, cudaStream_t st) {
-  auto go = [&](auto kernel, int cl) {
-    launch_scan(kernel, d, cl, st, d, (const T*)x, (const T*)gate, lengths, saved, (const T*)dh, dh_last, (T*)dx,
-                (T*)dgate, dh0, status);
-  };
+template <typename T, bool VEC, typename... A>
+int scan_bwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
+  constexpr int S = stages_of(3);
   switch (cluster_of(d)) {
-    case 1: return go(scan_bwd_kernel<T, VEC, 1>, 1);
-    case 2: return go(scan_bwd_kernel<T, VEC, 2>, 2);
-    case 4: return go(scan_bwd_kernel<T, VEC, 4>, 4);
-    default: return go(scan_bwd_kernel<T, VEC, 8>, 8);
+    case 1: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
+    case 2: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
+    case 4: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
+    default: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
   }
+}
+
+template <typename T>
+int fwd_of(bool vec, const frnnt_recurrence_dims& d, const void* x, const void* gate, const int32_t* lengths,
+           const float* h0, void* h, float* h_last, float* saved, int32_t* status, cudaStream_t st) {
+  return (vec ? scan_fwd<T, true, const T*, const T*, const int32_t*, const float*, T*, float*, float*, int32_t*>
+              : scan_fwd<T, false, const T*, const T*, const int32_t*, const float*, T*, float*, float*, int32_t*>)(
+      d, st, (const T*)x, (const T*)gate, lengths, h0, (T*)h, h_last, saved, status);
+}
+template <typename T>
+int bwd_of(bool vec, const frnnt_recurrence_dims& d, const void* x, const void* gate, const int32_t* lengths,
+           const float* saved, const void* dh, const float* dh_last, void* dx, void* dgate, float* dh0,
+           int32_t* status, cudaStream_t st) {
+  return (vec ? scan_bwd<T, true, const T*, const T*, const int32_t*, const float*, const T*, const float*, T*, T*,
+                         float*, int32_t*>
+              : scan_bwd<T, false, const T*, const T*, const int32_t*, const float*, const T*, const float*, T*, T*,
+                         float*, int32_t*>)(d, st, (const T*)x, (const T*)gate, lengths, saved, (const T*)dh, dh_last,
+                                            (T*)dx, (T*)dgate, dh0, status);
 }
 
 }  // namespace
@@ -456,10 +561,10 @@ extern "C" FRNNT_API int frnnt_recurrence_fwd(const frnnt_recurrence_dims* d, co
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("recurrence_fwd", st);
-    const bool vec = pairs_ok(*d, {x, gate, h}, {d->x_sb, d->x_st, d->gate_sb, d->gate_st, d->h_sb, d->h_st});
-    const bool bf = d->dtype == FRNNT_BF16;
-    (bf ? vec ? scan_fwd<__nv_bfloat16, true> : scan_fwd<__nv_bfloat16, false>
-        : vec ? scan_fwd<float, true> : scan_fwd<float, false>)(*d, x, gate, lengths, h0, h, h_last, saved, status, st);
+    const bool vec = vectors_ok(*d, {x, gate, h}, {d->x_sb, d->x_st, d->gate_sb, d->gate_st, d->h_sb, d->h_st});
+    const int rc = (d->dtype == FRNNT_BF16 ? fwd_of<__nv_bfloat16> : fwd_of<float>)(
+        vec, *d, x, gate, lengths, h0, h, h_last, saved, status, st);
+    if (rc) return rc;
   }
   return cudaGetLastError() == cudaSuccess ? FRNNT_OK : FRNNT_ERR_CUDA;
 }
@@ -479,13 +584,12 @@ extern "C" FRNNT_API int frnnt_recurrence_bwd(const frnnt_recurrence_dims* d, co
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("recurrence_bwd", st);
-    const bool vec = pairs_ok(*d, {x, gate, dh, dx, dgate},
+    const bool vec = vectors_ok(*d, {x, gate, dh, dx, dgate},
                               {d->x_sb, d->x_st, d->gate_sb, d->gate_st, d->dh_sb, d->dh_st, d->dx_sb, d->dx_st,
                                d->dgate_sb, d->dgate_st});
-    const bool bf = d->dtype == FRNNT_BF16;
-    (bf ? vec ? scan_bwd<__nv_bfloat16, true> : scan_bwd<__nv_bfloat16, false>
-        : vec ? scan_bwd<float, true> : scan_bwd<float, false>)(*d, x, gate, lengths, saved, dh, dh_last, dx, dgate,
-                                                                dh0, status, st);
+    const int rc = (d->dtype == FRNNT_BF16 ? bwd_of<__nv_bfloat16> : bwd_of<float>)(
+        vec, *d, x, gate, lengths, saved, dh, dh_last, dx, dgate, dh0, status, st);
+    if (rc) return rc;
   }
   return cudaGetLastError() == cudaSuccess ? FRNNT_OK : FRNNT_ERR_CUDA;
 }
