@@ -19,11 +19,6 @@ constexpr int kSteps = 16;
 constexpr int kWarps = kChunk / kSteps;
 constexpr int kTile = 64;
 static_assert(kWarps >= 8, "a warp for each block of a cluster");
-// Blocks an SM is to hold: shared memory and registers are dealt out for that.
-template <typename T>
-constexpr int blocks_of() {
-  return sizeof(T) == 2 ? 2 : 1;
-}
 
 // a = sigmoid(gate) and s = 1 - a = sigmoid(-gate), each to relative precision:
 // with e = exp(-gate), a = 1 / (1 + e), and s = e a where that is below 1/2 (1 -
@@ -197,7 +192,7 @@ struct Exchange<1> {
 // are too few (sequence, channel tile) pairs to fill the GPU, CL blocks of a
 // cluster take the chunks in turn.
 template <typename T, bool VEC, int CL, int STAGES>
-__global__ void __launch_bounds__(kWarps * 32, blocks_of<T>())
+__global__ void __launch_bounds__(kWarps * 32, 2)
     scan_fwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ h0, T* __restrict__ h,
                     float* __restrict__ h_last, float* __restrict__ saved, int32_t* status) {
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of<T>())
 // again from its saved state by the forward maps, in the same exchange, so x,
 // gate and dh are read once, dx and dgate written once, and h is not read.
 template <typename T, bool VEC, int CL, int STAGES>
-__global__ void __launch_bounds__(kWarps * 32, blocks_of<T>())
+__global__ void __launch_bounds__(kWarps * 32, 2)
     scan_bwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ saved, const T* __restrict__ dh,
                     const float* __restrict__ dh_last, T* __restrict__ dx, T* __restrict__ dgate,
@@ -470,22 +465,25 @@ int cluster_of(const frnnt_recurrence_dims& d) {
   return cl;
 }
 
-// Chunks in shared memory at a time: what leaves room for blocks_of<T>() blocks
-// on an SM (three of two arrays, two of three).
+// Chunks in shared memory at a time: three of two arrays, two of three (96 KB of
+// a 16-bit type: two blocks an SM; a block of a 32-bit type has the SM alone).
 constexpr int stages_of(int arrays) { return arrays == 2 ? 3 : 2; }
 
 template <typename T, int ARRAYS, auto kernel, typename... A>
 int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
-  constexpr int bytes = (int)sizeof(Stage<T>) * ARRAYS * stages_of(ARRAYS);
+  constexpr int chunk = (int)sizeof(Stage<T>) * ARRAYS, most = chunk * stages_of(ARRAYS);
   static std::atomic<bool> ready[kDeviceSlots];
   std::atomic<bool>& here = ready[current_device()];
   if (!here.load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
       return FRNNT_ERR_CUDA;
     here.store(true, std::memory_order_release);
   }
   const int warps = d.T < kChunk ? (d.T + kSteps - 1) / kSteps : kWarps;
   const dim3 grid((d.D + kTile - 1) / kTile * cl, d.B);
+  // one round needs one chunk's memory, and a short one only its rows
+  const int rounds = ((d.T + kChunk - 1) / kChunk + cl - 1) / cl;
+  const int bytes = rounds >= stages_of(ARRAYS) ? most : rounds * chunk;
   launch_k(kernel, grid, dim3(warps * 32), bytes, st, cl, args...);
   note_launch();
   return FRNNT_OK;

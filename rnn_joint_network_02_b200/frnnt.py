@@ -448,7 +448,10 @@ def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durati
 
 
 # ------------------------------------------------------------------ operators beside the loss (include/frnnt_ops.h)
+# These calls can be a few microseconds long on the GPU, so the host side is kept short: each tensor is checked once,
+# nothing is built that the call does not need, and sizes go to torch.empty one by one (a tuple costs it 0.8 us more).
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
 def _float_type(name, t):
@@ -458,68 +461,51 @@ def _float_type(name, t):
         raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}") from None
 
 
-def _expect(name, t, shape, dtype, dense=True):
-    """Refuses a tensor of another shape, type or (``dense``) layout than the call needs."""
+def _expect(name, t, shape, dtype, dev, dense=True):
+    """Refuses a tensor of another shape, type, device or (``dense``) layout than the call needs."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
 
 
 def _rows(name, t):
     """Elements from one row of a [N, C] tensor to the next (its columns must be adjacent)."""
     N, C = t.shape
-    if C > 1 and t.stride(1) != 1:
+    sn, sc = t.stride()
+    if C > 1 and sc != 1:
         raise ValueError(f"the columns of {name} must be adjacent (stride 1)")
-    return t.stride(0) if N > 1 else max(C, t.stride(0))
+    return sn if N > 1 else max(C, sn)
 
 
 def _steps(name, t):
     """(sequence stride, step stride) of a [B, T, D] tensor (its channels must be adjacent)."""
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    sb, st, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
         raise ValueError(f"the channels of {name} must be adjacent (stride 1)")
-    return t.stride(0), t.stride(1)
+    return sb, st
 
 
-def _on_device(first, others):
-    """Every tensor on the CUDA device of ``first``; run after the shape checks."""
-    dev = first.device
+def _elsewhere(dev, stream):
+    """None where a call on ``dev`` is to be queued on the current stream of the
+    current device; otherwise a context that makes it so, for the call's
+    outputs (which then belong to that device and stream) and its launch."""
     if dev.type != "cuda":
         raise ValueError("the library computes on the GPU: pass CUDA tensors")
-    for name, t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
-    return dev
+    if stream is None:
+        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
-class _Queue:
-    """The stream a call is queued on, with its device (and, for a stream other
-    than the current one, that stream) current while outputs are allocated and
-    the call is made, so that both belong to the device and stream they are
-    used on."""
-
-    def __init__(self, dev, stream):
-        self.guards = []
-        if stream is None:
-            if torch.cuda.current_device() != dev.index:
-                self.guards.append(torch.cuda.device(dev))
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the call's tensors on {dev}")
-            self.guards.append(torch.cuda.stream(stream))
-            self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _queue(dev):
+    """The current stream's handle on the current device."""
+    return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _status(check, dev):
@@ -547,11 +533,11 @@ class LogProbs:
 
     def __init__(self, N, K, top, device):
         f32 = torch.float32
-        self.logp = torch.empty((N, K), dtype=f32, device=device) if K else None
+        self.logp = torch.empty(N, K, dtype=f32, device=device) if K else None
         self.entropy = torch.empty(N, dtype=f32, device=device)
         self.lse = torch.empty(N, dtype=f32, device=device)
-        self.top_logp = torch.empty((N, top), dtype=f32, device=device) if top else None
-        self.top_ids = torch.empty((N, top), dtype=torch.int32, device=device) if top else None
+        self.top_logp = torch.empty(N, top, dtype=f32, device=device) if top else None
+        self.top_ids = torch.empty(N, top, dtype=torch.int32, device=device) if top else None
 
 
 def _check_logprobs(logits, tokens, top):
@@ -564,22 +550,22 @@ def _check_logprobs(logits, tokens, top):
         if tokens.dim() != 2:
             raise ValueError("tokens must be [N, K]")
         K = tokens.shape[1]
-        _expect("tokens", tokens, (N, K), torch.int32)
+        _expect("tokens", tokens, (N, K), torch.int32, logits.device)
     if not 0 <= top <= min(V, MAX_TOP) or K > MAX_TOKENS:
         raise ValueError(f"at most {MAX_TOKENS} tokens and min(V, {MAX_TOP}) alternatives per row")
     return dt, N, V, K
 
 
-def _check_result(fwd, N, K, top):
+def _check_result(fwd, N, K, top, dev):
     f32 = torch.float32
-    for name, t, shape, dt in (("logp", fwd.logp, (N, K), f32), ("entropy", fwd.entropy, (N,), f32),
-                               ("lse", fwd.lse, (N,), f32), ("top_logp", fwd.top_logp, (N, top), f32),
-                               ("top_ids", fwd.top_ids, (N, top), torch.int32)):
-        if t is None:
-            if shape[-1] and len(shape) == 2:
-                raise ValueError(f"the result has no {name}")
-        else:
-            _expect(name, t, shape, dt)
+    for name, t, n, dt in (("logp", fwd.logp, K, f32), ("top_logp", fwd.top_logp, top, f32),
+                           ("top_ids", fwd.top_ids, top, torch.int32)):
+        if t is not None:
+            _expect(name, t, (N, n), dt, dev)
+        elif n:
+            raise ValueError(f"the result has no {name}")
+    _expect("entropy", fwd.entropy, (N,), f32, dev)
+    _expect("lse", fwd.lse, (N,), f32, dev)
 
 
 def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, check=True, stream=None) -> LogProbs:
@@ -592,19 +578,20 @@ def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, chec
     and tokens outside [0, V) raise FrnntStatusError."""
     dt, N, V, K = _check_logprobs(logits, tokens, top)
     ld = _rows("logits", logits)
+    dev = logits.device
     if out is not None:
-        _check_result(out, N, K, top)
-    dev = _on_device(logits, (("tokens", tokens),) if out is None else
-                     (("tokens", tokens), ("out", out.logp), ("out", out.entropy), ("out", out.lse),
-                      ("out", out.top_logp), ("out", out.top_ids)))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            out = LogProbs(N, K, top, dev)
-        status = _status(check, dev)
-        rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V), logits.data_ptr(), _at(tokens),
-                                        _at(out.logp), out.entropy.data_ptr(), out.lse.data_ptr(), _at(out.top_logp),
-                                        _at(out.top_ids), _at(status), q.handle)
-        _finish(rc, status)
+        _check_result(out, N, K, top, dev)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return token_logprobs(logits, tokens, top, out, check)
+    if out is None:
+        out = LogProbs(N, K, top, dev)
+    status = _status(check and K > 0, dev)
+    rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V), logits.data_ptr(), _at(tokens),
+                                    _at(out.logp), out.entropy.data_ptr(), out.lse.data_ptr(), _at(out.top_logp),
+                                    _at(out.top_ids), _at(status), _queue(dev))
+    _finish(rc, status)
     return out
 
 
@@ -618,23 +605,30 @@ def token_logprobs_bwd(logits, tokens, fwd: LogProbs, dlogp=None, dentropy=None,
     top = 0 if fwd.top_ids is None else fwd.top_ids.shape[-1]
     dt, N, V, K = _check_logprobs(logits, tokens, top)
     ld = _rows("logits", logits)
-    _check_result(fwd, N, K, top)
-    for name, t, shape in (("dlogp", dlogp, (N, K)), ("dentropy", dentropy, (N,)), ("dtop", dtop, (N, top))):
-        if t is not None:
-            _expect(name, t, shape, torch.float32)
+    dev = logits.device
+    _check_result(fwd, N, K, top, dev)
+    if dlogp is not None:
+        _expect("dlogp", dlogp, (N, K), torch.float32, dev)
+    if dentropy is not None:
+        _expect("dentropy", dentropy, (N,), torch.float32, dev)
+    if dtop is not None:
+        _expect("dtop", dtop, (N, top), torch.float32, dev)
     if out is not None:
-        _expect("out", out, (N, V), logits.dtype, dense=False)
-    dev = _on_device(logits, (("tokens", tokens), ("fwd", fwd.lse), ("fwd", fwd.entropy), ("fwd", fwd.top_ids),
-                              ("dlogp", dlogp), ("dentropy", dentropy), ("dtop", dtop), ("out", out)))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            out = torch.empty((N, V), dtype=logits.dtype, device=dev)
-        status = _status(check, dev)
-        rc = lib().frnnt_token_logprobs_bwd(LogprobDims(N, V, K, top, dt, ld, _rows("out", out)), logits.data_ptr(),
-                                            _at(tokens), fwd.lse.data_ptr(), fwd.entropy.data_ptr(), _at(fwd.top_ids),
-                                            _at(dlogp), _at(dentropy), _at(dtop), out.data_ptr(), _at(status),
-                                            q.handle)
-        _finish(rc, status)
+        _expect("out", out, (N, V), logits.dtype, dev, dense=False)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return token_logprobs_bwd(logits, tokens, fwd, dlogp, dentropy, dtop, out, check)
+    if out is None:
+        out = torch.empty(N, V, dtype=logits.dtype, device=dev)
+        ldd = V
+    else:
+        ldd = _rows("out", out)
+    status = _status(check, dev)
+    rc = lib().frnnt_token_logprobs_bwd(LogprobDims(N, V, K, top, dt, ld, ldd), logits.data_ptr(), _at(tokens),
+                                        fwd.lse.data_ptr(), fwd.entropy.data_ptr(), _at(fwd.top_ids), _at(dlogp),
+                                        _at(dentropy), _at(dtop), out.data_ptr(), _at(status), _queue(dev))
+    _finish(rc, status)
     return out
 
 
@@ -644,20 +638,23 @@ class Recurrence:
     __slots__ = ("h", "h_last", "saved")
 
     def __init__(self, B, T, D, dtype, device, save=True):
-        self.h = torch.empty((B, T, D), dtype=dtype, device=device)
-        self.h_last = torch.empty((B, D), dtype=torch.float32, device=device)
-        n = (T + SCAN_CHUNK - 1) // SCAN_CHUNK
-        self.saved = torch.empty((B, n, D), dtype=torch.float32, device=device) if save else None
+        self.h = torch.empty(B, T, D, dtype=dtype, device=device)
+        self.h_last = torch.empty(B, D, dtype=torch.float32, device=device)
+        self.saved = torch.empty(B, _marks(T), D, dtype=torch.float32, device=device) if save else None
+
+
+def _marks(T):
+    return (T + SCAN_CHUNK - 1) // SCAN_CHUNK
 
 
 def _check_recurrence(x, gate, lengths):
     if x.dim() != 3:
         raise ValueError("x and gate must be [B, T, D]")
     dt = _float_type("x", x)
-    _expect("gate", gate, x.shape, x.dtype, dense=False)
     B, T, D = x.shape
+    _expect("gate", gate, (B, T, D), x.dtype, x.device, dense=False)
     if lengths is not None:
-        _expect("lengths", lengths, (B,), torch.int32)
+        _expect("lengths", lengths, (B,), torch.int32, x.device)
     return dt, B, T, D
 
 
@@ -668,26 +665,31 @@ def recurrence(x, gate, lengths=None, h0=None, save=True, out: Recurrence | None
     and steps may be strided, as the halves of one projection are), from h0
     [B, D] (fp32; zero when None), each sequence to its length (int32 [B]; T
     when None; rows past it come back 0).  ``save`` keeps what recurrence_bwd
-    needs."""
+    needs.  ``out``: an earlier call's result, written again."""
     dt, B, T, D = _check_recurrence(x, gate, lengths)
+    dev = x.device
     if h0 is not None:
-        _expect("h0", h0, (B, D), torch.float32)
+        _expect("h0", h0, (B, D), torch.float32, dev)
     if out is not None:
-        _expect("out.h", out.h, x.shape, x.dtype, dense=False)
-        _expect("out.h_last", out.h_last, (B, D), torch.float32)
+        _expect("out.h", out.h, (B, T, D), x.dtype, dev, dense=False)
+        _expect("out.h_last", out.h_last, (B, D), torch.float32, dev)
         if out.saved is not None:
-            _expect("out.saved", out.saved, (B, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, D), torch.float32)
+            _expect("out.saved", out.saved, (B, _marks(T), D), torch.float32, dev)
     strides = _steps("x", x) + _steps("gate", gate)
-    others = (("gate", gate), ("lengths", lengths), ("h0", h0))
-    dev = _on_device(x, others if out is None else others + (("out", out.h), ("out", out.h_last), ("out", out.saved)))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            out = Recurrence(B, T, D, x.dtype, dev, save)
-        status = _status(check and lengths is not None, dev)
-        rc = lib().frnnt_recurrence_fwd(RecurrenceDims(B, T, D, dt, *strides, *_steps("out.h", out.h)), x.data_ptr(),
-                                        gate.data_ptr(), _at(lengths), _at(h0), out.h.data_ptr(),
-                                        out.h_last.data_ptr(), _at(out.saved), _at(status), q.handle)
-        _finish(rc, status)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return recurrence(x, gate, lengths, h0, save, out, check)
+    if out is None:
+        out = Recurrence(B, T, D, x.dtype, dev, save)
+        strides += (T * D, D)
+    else:
+        strides += _steps("out.h", out.h)
+    status = _status(check and lengths is not None, dev)
+    rc = lib().frnnt_recurrence_fwd(RecurrenceDims(B, T, D, dt, *strides), x.data_ptr(), gate.data_ptr(),
+                                    _at(lengths), _at(h0), out.h.data_ptr(), out.h_last.data_ptr(), _at(out.saved),
+                                    _at(status), _queue(dev))
+    _finish(rc, status)
     return out
 
 
@@ -699,30 +701,35 @@ def recurrence_bwd(x, gate, fwd: Recurrence, dh, lengths=None, dh_last=None, out
     and lengths.  ``out``: a dict with dx, dgate and dh0 to write to (dx and
     dgate may be the halves of one gradient)."""
     dt, B, T, D = _check_recurrence(x, gate, lengths)
+    dev = x.device
     if fwd.saved is None:
         raise ValueError("the forward call kept no states (save=False)")
-    _expect("fwd.saved", fwd.saved, (B, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, D), torch.float32)
-    _expect("dh", dh, x.shape, x.dtype, dense=False)
+    _expect("fwd.saved", fwd.saved, (B, _marks(T), D), torch.float32, dev)
+    _expect("dh", dh, (B, T, D), x.dtype, dev, dense=False)
     if dh_last is not None:
-        _expect("dh_last", dh_last, (B, D), torch.float32)
+        _expect("dh_last", dh_last, (B, D), torch.float32, dev)
     if out is not None:
-        _expect("out dx", out["dx"], x.shape, x.dtype, dense=False)
-        _expect("out dgate", out["dgate"], x.shape, x.dtype, dense=False)
-        _expect("out dh0", out["dh0"], (B, D), torch.float32)
+        _expect("out dx", out["dx"], (B, T, D), x.dtype, dev, dense=False)
+        _expect("out dgate", out["dgate"], (B, T, D), x.dtype, dev, dense=False)
+        _expect("out dh0", out["dh0"], (B, D), torch.float32, dev)
     strides = _steps("x", x) + _steps("gate", gate) + (0, 0) + _steps("dh", dh)
-    others = (("gate", gate), ("lengths", lengths), ("fwd", fwd.saved), ("dh", dh), ("dh_last", dh_last))
-    dev = _on_device(x, others if out is None else others + tuple(("out", t) for t in out.values()))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            out = dict(dx=torch.empty((B, T, D), dtype=x.dtype, device=dev),
-                       dgate=torch.empty((B, T, D), dtype=x.dtype, device=dev),
-                       dh0=torch.empty((B, D), dtype=torch.float32, device=dev))
-        status = _status(check and lengths is not None, dev)
-        dims = RecurrenceDims(B, T, D, dt, *strides, *_steps("out dx", out["dx"]), *_steps("out dgate", out["dgate"]))
-        rc = lib().frnnt_recurrence_bwd(dims, x.data_ptr(), gate.data_ptr(), _at(lengths), fwd.saved.data_ptr(),
-                                        dh.data_ptr(), _at(dh_last), out["dx"].data_ptr(), out["dgate"].data_ptr(),
-                                        out["dh0"].data_ptr(), _at(status), q.handle)
-        _finish(rc, status)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return recurrence_bwd(x, gate, fwd, dh, lengths, dh_last, out, check)
+    if out is None:
+        out = dict(dx=torch.empty(B, T, D, dtype=x.dtype, device=dev),
+                   dgate=torch.empty(B, T, D, dtype=x.dtype, device=dev),
+                   dh0=torch.empty(B, D, dtype=torch.float32, device=dev))
+        strides += (T * D, D, T * D, D)
+    else:
+        strides += _steps("out dx", out["dx"]) + _steps("out dgate", out["dgate"])
+    status = _status(check and lengths is not None, dev)
+    rc = lib().frnnt_recurrence_bwd(RecurrenceDims(B, T, D, dt, *strides), x.data_ptr(), gate.data_ptr(),
+                                    _at(lengths), fwd.saved.data_ptr(), dh.data_ptr(), _at(dh_last),
+                                    out["dx"].data_ptr(), out["dgate"].data_ptr(), out["dh0"].data_ptr(),
+                                    _at(status), _queue(dev))
+    _finish(rc, status)
     return out
 
 
@@ -735,37 +742,37 @@ def recurrence_step(x, gate, state, parent=None, advance=None, out=None, check=T
     if x.dim() != 2 or state.dim() != 2:
         raise ValueError("x and gate must be [N, D] and state [S, D]")
     dt = _float_type("x", x)
-    _expect("gate", gate, x.shape, x.dtype, dense=False)
+    dev = x.device
     N, D = x.shape
     S = state.shape[0]
-    _expect("state", state, (S, D), torch.float32)
+    _expect("gate", gate, (N, D), x.dtype, dev, dense=False)
+    _expect("state", state, (S, D), torch.float32, dev)
     if parent is not None:
-        _expect("parent", parent, (N,), torch.int32)
+        _expect("parent", parent, (N,), torch.int32, dev)
     elif N > S:
         raise ValueError(f"{N} rows need parents among the {S} rows of state")
     if advance is not None:
-        _expect("advance", advance, (N,), torch.bool)
+        _expect("advance", advance, (N,), torch.bool, dev)
     x_sn, gate_sn = _rows("x", x), _rows("gate", gate)
-    h = new = None
     if out is not None:
         h, new = out
-        _expect("out h", h, (N, D), x.dtype)
-        _expect("out state", new, (N, D), torch.float32)
-        if parent is not None or new.data_ptr() != state.data_ptr():
-            lo, hi = state.data_ptr(), state.data_ptr() + S * D * 4
-            if new.data_ptr() < hi and lo < new.data_ptr() + N * D * 4:
-                raise ValueError("the new state overlaps the old one, which other rows still read")
-    dev = _on_device(x, (("gate", gate), ("state", state), ("parent", parent), ("advance", advance), ("out", h),
-                         ("out", new)))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            h = torch.empty((N, D), dtype=x.dtype, device=dev)
-            new = torch.empty((N, D), dtype=torch.float32, device=dev)
-        status = _status(check and parent is not None, dev)
-        rc = lib().frnnt_recurrence_step(StepDims(N, S, D, dt, x_sn, gate_sn), x.data_ptr(), gate.data_ptr(),
-                                         state.data_ptr(), _at(parent), _at(advance), h.data_ptr(), new.data_ptr(),
-                                         _at(status), q.handle)
-        _finish(rc, status)
+        _expect("out h", h, (N, D), x.dtype, dev)
+        _expect("out state", new, (N, D), torch.float32, dev)
+        old, at = state.data_ptr(), new.data_ptr()
+        if (parent is not None or at != old) and at < old + S * D * 4 and old < at + N * D * 4:
+            raise ValueError("the new state overlaps the old one, which other rows still read")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return recurrence_step(x, gate, state, parent, advance, out, check)
+    if out is None:
+        h = torch.empty(N, D, dtype=x.dtype, device=dev)
+        new = torch.empty(N, D, dtype=torch.float32, device=dev)
+    status = _status(check and parent is not None, dev)
+    rc = lib().frnnt_recurrence_step(StepDims(N, S, D, dt, x_sn, gate_sn), x.data_ptr(), gate.data_ptr(),
+                                     state.data_ptr(), _at(parent), _at(advance), h.data_ptr(), new.data_ptr(),
+                                     _at(status), _queue(dev))
+    _finish(rc, status)
     return h, new
 
 
@@ -798,18 +805,19 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
     to ``offset`` (a captured graph then draws new numbers at each replay).
     ``out`` may be x."""
     dt = _float_type("x", x)
+    dev = x.device
     if x.numel() == 0:
         raise ValueError("x has no elements")
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1], not {p}")
-    rng = None
+    rng, key = None, seed
     if isinstance(seed, torch.Tensor):
-        rng, seed = seed, 0
-        _expect("seed", rng, (2,), torch.int64)
+        rng, key = seed, 0
+        _expect("seed", rng, (2,), torch.int64, dev)
     R, C, x_ld = _matrix("x", x)
     y_ld = C
     if out is not None:
-        _expect("out", out, x.shape, x.dtype, dense=False)
+        _expect("out", out, x.shape, x.dtype, dev, dense=False)
         Ry, Cy, y_ld = _matrix("out", out)
         if (R, C) != (Ry, Cy):     # one of the two is contiguous: take the rows of the other
             if R == 1:
@@ -818,12 +826,14 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
                 y_ld = C
             else:
                 raise ValueError("x and out have rows of different lengths")
-    dev = _on_device(x, (("seed", rng), ("out", out)))
-    with _Queue(dev, stream) as q:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        mask = (1 << 64) - 1
-        rc = lib().frnnt_dropout(DropoutDims(R, C, dt, x_ld, y_ld, p, seed & mask, offset & mask), x.data_ptr(),
-                                 out.data_ptr(), _at(rng), q.handle)
-        _finish(rc, None)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return dropout(x, p, seed, offset, out)
+    if out is None:
+        out = torch.empty_like(x) if R == 1 else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    mask = (1 << 64) - 1
+    rc = lib().frnnt_dropout(DropoutDims(R, C, dt, x_ld, y_ld, p, key & mask, offset & mask), x.data_ptr(),
+                             out.data_ptr(), _at(rng), _queue(dev))
+    _finish(rc, None)
     return out
