@@ -84,7 +84,8 @@ typedef struct {
   int B, T, D;               /* sequences, steps, channels (all >= 1)                          */
   frnnt_dtype dtype;         /* element type of x, gate, h, dh, dx and dgate                   */
   /* strides in elements from one sequence (_sb) and one step (_st) to the next; channels are contiguous.
-   * Inputs: any strides >= 0.  Outputs (h, dx, dgate): no two elements may share an address.   */
+   * Inputs: any strides >= 0, a step at most 2^30 elements.  Outputs (h, dx, dgate): no two elements may
+   * share an address.                                                                          */
   long long x_sb, x_st, gate_sb, gate_st, h_sb, h_st;
   long long dh_sb, dh_st, dx_sb, dx_st, dgate_sb, dgate_st;   /* backward only                  */
 } frnnt_recurrence_dims;

@@ -11,13 +11,12 @@
 namespace frnnt {
 namespace {
 
-// A block walks along one sequence, kTile channels wide, kChunk steps at a
+// A block walks along one sequence, 64 channels wide, kChunk steps at a
 // time.  Lane l of every warp holds channels 2l and 2l + 1; warp w takes the
 // kSteps steps from w * kSteps on.
 constexpr int kChunk = FRNNT_SCAN_CHUNK;
 constexpr int kSteps = 16;
 constexpr int kWarps = kChunk / kSteps;
-constexpr int kTile = 64;
 static_assert(kWarps >= 8, "a warp for each block of a cluster");
 
 // a = sigmoid(gate) and s = 1 - a = sigmoid(-gate), each to relative precision:
@@ -70,43 +69,70 @@ struct Pair<__nv_bfloat16> {
   }
 };
 
-// One array of a chunk in shared memory: kChunk steps of kTile channels.
+// One array of a chunk in shared memory: kChunk rows of kPitch elements.
+// VEC: every row of the array starts on a 16-byte boundary.  Otherwise a row is
+// copied from the boundary at or before it (which lies in the same
+// allocation: those start on 256-byte boundaries) and read at that offset, and
+// a block takes 16 bytes' worth of channels less, so that the row still fits.
+constexpr int kPitch = 64;
+template <typename T, bool VEC>
+constexpr int kTile = VEC ? kPitch : kPitch - 16 / (int)sizeof(T);
+
 template <typename T>
 struct Stage {
-  T v[kChunk][kTile];
-  __device__ __forceinline__ uint64_t at(int t, int lane) const {
-    return Pair<T>::open(reinterpret_cast<const typename Pair<T>::Raw*>(v[t])[lane]);
-  }
+  T v[kChunk][kPitch];
 };
 
-// Copies rows t0 .. t0 + 16 warps - 1 (those in [0, len)) of channels c0 ..
-// into `to`.  VEC: the rows start on 16-byte boundaries and are copied
-// asynchronously, 16 bytes a thread; otherwise element by element.
+// Rows t0 .. of one array, from channel c0 on.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_stage(Stage<T>& to, const T* __restrict__ p, long long step, int t0, int len,
-                                           int c0, int D) {
-  if (VEC) {
-    constexpr int E = 16 / sizeof(T), kPerRow = kTile / E;
-    const int j = threadIdx.x % kPerRow, c = c0 + j * E;
-    const int rows = blockDim.x / kPerRow, bytes = min(E, D - c) * (int)sizeof(T);
-    if (c >= D) return;
-    const int first = threadIdx.x / kPerRow;
-    const T* src = p + (t0 + first) * step + c;
-    uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&to.v[first][j * E]));
+struct Rows {
+  const char* first;   // of step 0
+  long long step;      // bytes
+  int width;           // bytes of a row that exist
+  __device__ __forceinline__ Rows(const T* p, long long step_elems, int c0, int D)
+      : first(reinterpret_cast<const char*>(p + c0)), step(step_elems * (long long)sizeof(T)),
+        width(min(kTile<T, VEC>, D - c0) * (int)sizeof(T)) {}
+
+  // Starts the copy of the block's rows t0 .. (16 a warp) into `to`; rows from
+  // len on get `rest` (two 16-bit values or one 32-bit one).
+  __device__ __forceinline__ void fetch(Stage<T>& to, int t0, int len, uint32_t rest) const {
+    constexpr int kPerRow = kPitch * sizeof(T) / 16, kTimes = kSteps * kPerRow / 32;
+    const int j = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow, rows = blockDim.x / kPerRow;
+    const char* src = first + (t0 + r0) * step;
+    uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to.v[r0])) + 16 * j;
+    const long long skip = rows * step;
+    const int left = len - t0 - r0;
+    if (len - t0 >= kTimes * rows) {
 #pragma unroll
-    for (int k = 0; k < kSteps * kPerRow / 32; ++k) {
-      if (t0 + first + k * rows < len)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-      src += rows * step;
-      dst += rows * kTile * sizeof(T);
-    }
-  } else {
-    for (int i = threadIdx.x; i < (int)(blockDim.x / 32) * kSteps * kTile; i += blockDim.x) {
-      const int t = i / kTile, c = i % kTile;
-      if (t0 + t < len && c0 + c < D) to.v[t][c] = p[(t0 + t) * step + c0 + c];
+      for (int k = 0; k < kTimes; ++k) copy(dst + k * rows * (uint32_t)sizeof(to.v[0]), src + k * skip, j);
+    } else {
+      for (int k = 0; k < kTimes; ++k, src += skip, dst += rows * (uint32_t)sizeof(to.v[0])) {
+        if (k * rows < left) copy(dst, src, j);
+        else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(rest) : "memory");
+      }
     }
   }
-}
+  __device__ __forceinline__ void copy(uint32_t dst, const char* row, int j) const {
+    const int skew = VEC ? 0 : (int)((uintptr_t)row & 15);
+    const int bytes = min(16, width + skew - 16 * j);
+    if (bytes > 0)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(row - skew + 16 * j), "r"(bytes)
+                   : "memory");
+  }
+  // Where row t0 + i of the stage starts, for read().
+  __device__ __forceinline__ uint32_t skew(int t0) const { return VEC ? 0u : (uint32_t)(uintptr_t)(first + t0 * step); }
+  // The lane's two channels of row w0 + i; skew0: skew() of row w0.
+  __device__ __forceinline__ uint64_t read(const Stage<T>& from, int w0, int i, int lane, uint32_t skew0) const {
+    if (VEC) return Pair<T>::open(reinterpret_cast<const typename Pair<T>::Raw*>(from.v[w0 + i])[lane]);
+    const int off = (int)((skew0 + (uint32_t)i * (uint32_t)step) & 15u) / (int)sizeof(T) + 2 * lane;
+    // (the last lanes' channels are past the tile: any value does)
+    const T* q = from.v[w0 + i] + min(off, kPitch - 2);
+    return f2_of(to_f32<T>(q[0]), to_f32<T>(q[1]));
+  }
+};
+// Neutral rows: with gate = +inf, a = 1 and 1 - a = 0, and the state stays as it is.
+template <typename T>
+constexpr uint32_t kOpen = sizeof(T) == 4 ? 0x7F800000u : 0x7F807F80u;
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_pair(T* p, float2 v, bool two) {
@@ -202,20 +228,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c0 = (blockIdx.x / CL) * kTile, c = c0 + 2 * lane;
-  const bool live = c < d.D, two = c + 1 < d.D;
+  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
+  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
-  const T* xp = x + b * d.x_sb;
-  const T* gp = gate + b * d.gate_sb;
+  const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D);
   T* hp = h + b * d.h_sb + c;
   ex.init();
   if (CL > 1) cluster_arrive();
   auto fetch = [&](int r) {
     if (r < rounds) {
       const int t = (r * CL + rank) * kChunk;
-      load_stage<T, VEC>(stage[2 * (r % STAGES)], xp, d.x_st, t, len, c0, d.D);
-      load_stage<T, VEC>(stage[2 * (r % STAGES) + 1], gp, d.gate_st, t, len, c0, d.D);
+      xs.fetch(stage[2 * (r % STAGES)], t, len, 0u);
+      gs.fetch(stage[2 * (r % STAGES) + 1], t, len, kOpen<T>);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -229,22 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     __syncthreads();              // this round's rows are here; the stage before is free
     fetch(r + STAGES - 1);
     const Stage<T>&sx = stage[2 * (r % STAGES)], &sg = stage[2 * (r % STAGES) + 1];
+    const uint32_t xk = xs.skew(t0), gk = gs.skew(t0);
     uint64_t a[kSteps], v[kSteps];
     Map m = map_one();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const Gates g = gates_of(sg.at(w * kSteps + i, lane));
+      const Gates g = gates_of(gs.read(sg, w * kSteps, i, lane, gk));
       a[i] = g.a;
-      v[i] = f2_mul(g.s, sx.at(w * kSteps + i, lane));
-    }
-    const bool whole = t0 + kSteps <= len;
-    if (!whole) {                 // steps past the sequence leave the state as it is
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (t0 + i >= len) {
-          a[i] = f2_of(1.f, 1.f);
-          v[i] = f2_of(0.f, 0.f);
-        }
+      v[i] = f2_mul(g.s, xs.read(sx, w * kSteps, i, lane, xk));
     }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) m = then(m, Map{a[i], v[i]});
@@ -269,18 +286,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     if (w == 0 && t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
     uint64_t s = apply(before, in);
-    T* q = hp + t0 * d.h_st;
-    if (whole) {
+    T* out = hp + (long long)t0 * d.h_st;
+    if (t0 + kSteps <= len) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i, q += d.h_st) {
+      for (int i = 0; i < kSteps; ++i, out += d.h_st) {
         s = f2_fma(a[i], s, v[i]);
-        if (live) store_pair<T, VEC>(q, f2_open(s), two);
+        if (live) store_pair<T, VEC>(out, f2_open(s), two);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i, q += d.h_st) {
+      for (int i = 0; i < kSteps; ++i, out += d.h_st) {
         s = f2_fma(a[i], s, v[i]);
-        if (live && t0 + i < d.T) store_pair<T, VEC>(q, t0 + i < len ? f2_open(s) : make_float2(0.f, 0.f), two);
+        if (live && t0 + i < d.T)
+          store_pair<T, VEC>(out, t0 + i < len ? f2_open(s) : make_float2(0.f, 0.f), two);
       }
     }
   }
@@ -308,13 +326,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c0 = (blockIdx.x / CL) * kTile, c = c0 + 2 * lane;
-  const bool live = c < d.D, two = c + 1 < d.D;
+  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
+  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
-  const T* xp = x + b * d.x_sb;
-  const T* gp = gate + b * d.gate_sb;
-  const T* hp = dh + b * d.dh_sb;
+  const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D),
+      hs(dh + b * d.dh_sb, d.dh_st, c0, d.D);
   T* dxp = dx + b * d.dx_sb + c;
   T* dgp = dgate + b * d.dgate_sb + c;
   ex.init();
@@ -325,9 +342,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if (r < rounds) {
       const int t = chunk_at(r);
       Stage<T>* to = stage + 3 * (r % STAGES);
-      load_stage<T, VEC>(to[0], xp, d.x_st, t, len, c0, d.D);
-      load_stage<T, VEC>(to[1], gp, d.gate_st, t, len, c0, d.D);
-      load_stage<T, VEC>(to[2], hp, d.dh_st, t, len, c0, d.D);
+      xs.fetch(to[0], t, len, 0u);
+      gs.fetch(to[1], t, len, kOpen<T>);
+      hs.fetch(to[2], t, len, 0u);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -342,23 +359,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     __syncthreads();              // this round's rows are here; the stage before is free
     fetch(r + STAGES - 1);
     const Stage<T>* at = stage + 3 * (r % STAGES);
+    const uint32_t xk = xs.skew(t0), gk = gs.skew(t0), hk = hs.skew(t0);
     uint64_t a[kSteps], s[kSteps], past[kSteps];
     Map m = map_one();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const Gates g = gates_of(at[1].at(w * kSteps + i, lane));
+      const Gates g = gates_of(gs.read(at[1], w * kSteps, i, lane, gk));
       a[i] = g.a;
       s[i] = g.s;
     }
-    const bool whole = t0 + kSteps <= len;
-    const int n = whole ? kSteps : max(0, len - t0);   // steps within the sequence
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-      if (whole || i < n) m = then(m, Map{a[i], f2_mul(s[i], at[0].at(w * kSteps + i, lane))});
+    for (int i = 0; i < kSteps; ++i) m = then(m, Map{a[i], f2_mul(s[i], xs.read(at[0], w * kSteps, i, lane, xk))});
     uint64_t q = f2_of(0.f, 0.f);
 #pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i)
-      if (whole || i < n) q = f2_mul(a[i], f2_add(q, at[2].at(w * kSteps + i, lane)));
+    for (int i = kSteps - 1; i >= 0; --i) q = f2_mul(a[i], f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk)));
     run[w][lane] = make_ulonglong2(m.A, m.R);
     back[w][lane] = q;
     __syncthreads();
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if constexpr (CL > 1) ex.send(r, rank, lane, w, all);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {   // the states again, while the maps travel
-      const uint64_t xv = at[0].at(w * kSteps + i, lane);
+      const uint64_t xv = xs.read(at[0], w * kSteps, i, lane, xk);
       past[i] = f2_fma(xv, f2_of(-1.f, -1.f), v);
       v = f2_fma(a[i], v, f2_mul(s[i], xv));
     }
@@ -383,18 +397,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     q = apply(after, in);
     T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
     T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
+    if (t0 + kSteps <= len) {
 #pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
-      if (whole || i < n) {
-        const uint64_t g = f2_add(q, at[2].at(w * kSteps + i, lane));
+      for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
+        const uint64_t g = f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk));
         q = f2_mul(a[i], g);
         if (live) {
           store_pair<T, VEC>(px, f2_open(f2_mul(s[i], g)), two);
           store_pair<T, VEC>(pg, f2_open(f2_mul(f2_mul(q, s[i]), past[i])), two);
         }
-      } else if (live && t0 + i < d.T) {
-        store_pair<T, VEC>(px, make_float2(0.f, 0.f), two);
-        store_pair<T, VEC>(pg, make_float2(0.f, 0.f), two);
+      }
+    } else {
+#pragma unroll
+      for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
+        const uint64_t g = f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk));
+        q = f2_mul(a[i], g);
+        if (live && t0 + i < d.T) {
+          const bool on = t0 + i < len;
+          const float2 zero = make_float2(0.f, 0.f);
+          store_pair<T, VEC>(px, on ? f2_open(f2_mul(s[i], g)) : zero, two);
+          store_pair<T, VEC>(pg, on ? f2_open(f2_mul(f2_mul(q, s[i]), past[i])) : zero, two);
+        }
       }
     }
   }
@@ -429,9 +452,8 @@ __global__ void step_kernel(frnnt_step_dims d, const T* x, const T* gate, const 
 
 bool dtype_ok(frnnt_dtype t) { return t == FRNNT_F32 || t == FRNNT_BF16; }
 
-constexpr long long kMaxStride = 1LL << 40;
-
-bool in_strides_ok(long long sb, long long st) { return sb >= 0 && st >= 0 && sb <= kMaxStride && st <= kMaxStride; }
+// (the kernels hold step strides in 32 bits)
+bool in_strides_ok(long long sb, long long st) { return sb >= 0 && st >= 0 && sb <= (1LL << 40) && st <= (1LL << 30); }
 
 // No two of the B x T rows of D elements share an address: sequence-major or
 // step-major, with any gaps.
@@ -457,11 +479,12 @@ bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 size_t size_of(frnnt_dtype t) { return t == FRNNT_BF16 ? 2 : 4; }
 
 // Blocks that share a sequence's chunks.
-int cluster_of(const frnnt_recurrence_dims& d) {
-  const long long tiles = (long long)((d.D + kTile - 1) / kTile) * d.B;
+int cluster_of(const frnnt_recurrence_dims& d, int tile) {
+  const long long tiles = (long long)((d.D + tile - 1) / tile) * d.B;
   const int nc = (d.T + kChunk - 1) / kChunk;
+  const int fill = d.dtype == FRNNT_BF16 ? 148 : 74;
   int cl = 1;
-  while (cl < 8 && cl < nc && tiles * cl < 148) cl *= 2;
+  while (cl < 8 && cl < nc && tiles * cl < fill) cl *= 2;
   return cl;
 }
 
@@ -469,7 +492,7 @@ int cluster_of(const frnnt_recurrence_dims& d) {
 // a 16-bit type: two blocks an SM; a block of a 32-bit type has the SM alone).
 constexpr int stages_of(int arrays) { return arrays == 2 ? 3 : 2; }
 
-template <typename T, int ARRAYS, auto kernel, typename... A>
+template <typename T, int TILE, int ARRAYS, auto kernel, typename... A>
 int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
   constexpr int chunk = (int)sizeof(Stage<T>) * ARRAYS, most = chunk * stages_of(ARRAYS);
   static std::atomic<bool> ready[kDeviceSlots];
@@ -480,7 +503,7 @@ int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... ar
     here.store(true, std::memory_order_release);
   }
   const int warps = d.T < kChunk ? (d.T + kSteps - 1) / kSteps : kWarps;
-  const dim3 grid((d.D + kTile - 1) / kTile * cl, d.B);
+  const dim3 grid((d.D + TILE - 1) / TILE * cl, d.B);
   // one round needs one chunk's memory, and a short one only its rows
   const int rounds = ((d.T + kChunk - 1) / kChunk + cl - 1) / cl;
   const int bytes = rounds >= stages_of(ARRAYS) ? most : rounds * chunk;
@@ -503,22 +526,22 @@ bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void
 template <typename T, bool VEC, typename... A>
 int scan_fwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
   constexpr int S = stages_of(2);
-  switch (cluster_of(d)) {
-    case 1: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
-    case 2: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
-    case 4: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
-    default: return launch_scan<T, 2, scan_fwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
+  switch (cluster_of(d, kTile<T, VEC>)) {
+    case 1: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
+    case 2: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
+    case 4: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
+    default: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
   }
 }
 
 template <typename T, bool VEC, typename... A>
 int scan_bwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
   constexpr int S = stages_of(3);
-  switch (cluster_of(d)) {
-    case 1: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
-    case 2: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
-    case 4: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
-    default: return launch_scan<T, 3, scan_bwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
+  switch (cluster_of(d, kTile<T, VEC>)) {
+    case 1: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
+    case 2: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
+    case 4: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
+    default: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
   }
 }
 
@@ -597,7 +620,7 @@ extern "C" FRNNT_API int frnnt_recurrence_step(const frnnt_step_dims* d, const v
                                                void* h, float* new_state, int32_t* status, void* stream) {
   if (!d) return FRNNT_ERR_NULL;
   if (!dtype_ok(d->dtype)) return FRNNT_ERR_UNSUPPORTED;
-  if (d->N < 1 || d->N > 65535 || d->S < 1 || d->D < 1 || !in_strides_ok(d->x_sn, d->gate_sn) ||
+  if (d->N < 1 || d->N > 65535 || d->S < 1 || d->D < 1 || d->x_sn < 0 || d->gate_sn < 0 ||
       (!parent && d->N > d->S) || (parent && new_state == state))
     return FRNNT_ERR_DIMS;
   if (!x || !gate || !state || !h || !new_state) return FRNNT_ERR_NULL;
