@@ -103,8 +103,18 @@ struct Rows {
     const long long skip = rows * step;
     const int left = len - t0 - r0;
     if (len - t0 >= kTimes * rows) {
+      if (VEC) {
+        const int bytes = max(0, min(16, width - 16 * j));
+        src = bytes > 0 ? src + 16 * j : first;
 #pragma unroll
-      for (int k = 0; k < kTimes; ++k) copy(dst + k * rows * (uint32_t)sizeof(to.v[0]), src + k * skip, j);
+        for (int k = 0; k < kTimes; ++k, src += skip, dst += rows * (uint32_t)sizeof(to.v[0]))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(bytes > 0 ? src : first),
+                       "r"(bytes)
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTimes; ++k) copy(dst + k * rows * (uint32_t)sizeof(to.v[0]), src + k * skip, j);
+      }
     } else {
       for (int k = 0; k < kTimes; ++k, src += skip, dst += rows * (uint32_t)sizeof(to.v[0])) {
         if (k * rows < left) copy(dst, src, j);
@@ -114,10 +124,9 @@ struct Rows {
   }
   __device__ __forceinline__ void copy(uint32_t dst, const char* row, int j) const {
     const int skew = VEC ? 0 : (int)((uintptr_t)row & 15);
-    const int bytes = min(16, width + skew - 16 * j);
-    if (bytes > 0)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(row - skew + 16 * j), "r"(bytes)
-                   : "memory");
+    const int bytes = max(0, min(16, width + skew - 16 * j));   // 0: zeros, nothing is read
+    const char* src = bytes > 0 ? row - skew + 16 * j : first;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   }
   // Where row t0 + i of the stage starts, for read().
   __device__ __forceinline__ uint32_t skew(int t0) const { return VEC ? 0u : (uint32_t)(uintptr_t)(first + t0 * step); }
@@ -134,6 +143,11 @@ struct Rows {
 template <typename T>
 constexpr uint32_t kOpen = sizeof(T) == 4 ? 0x7F800000u : 0x7F807F80u;
 
+// A pair at a 32-bit byte offset from a block-wide base.
+template <typename T>
+__device__ __forceinline__ void store_at(char* base, uint32_t off, uint64_t v) {
+  *reinterpret_cast<typename Pair<T>::Raw*>(base + off) = Pair<T>::pack(f2_open(v));
+}
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_pair(T* p, float2 v, bool two) {
   using Raw = typename Pair<T>::Raw;
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
   const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
-  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D;
+  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D, whole = c0 + kPitch <= d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
   const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D);
@@ -286,14 +300,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     if (w == 0 && t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
     uint64_t s = apply(before, in);
-    T* out = hp + (long long)t0 * d.h_st;
-    if (t0 + kSteps <= len) {
+    if (VEC && whole && t0 + kSteps <= len) {
+      char* base = reinterpret_cast<char*>(h + b * d.h_sb + c0 + (long long)(r * CL + rank) * kChunk * d.h_st);
+      const uint32_t step = (uint32_t)d.h_st * (uint32_t)sizeof(T);
+      uint32_t off = w * kSteps * step + lane * 2 * (uint32_t)sizeof(T);
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i, out += d.h_st) {
+      for (int i = 0; i < kSteps; ++i, off += step) {
         s = f2_fma(a[i], s, v[i]);
-        if (live) store_pair<T, VEC>(out, f2_open(s), two);
+        store_at<T>(base, off, s);
       }
     } else {
+      T* out = hp + (long long)t0 * d.h_st;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i, out += d.h_st) {
         s = f2_fma(a[i], s, v[i]);
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
   const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
-  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D;
+  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D, whole = c0 + kPitch <= d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
   const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D),
@@ -395,19 +412,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, status);
     else carry = apply(all, carry);
     q = apply(after, in);
-    T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
-    T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
-    if (t0 + kSteps <= len) {
+    if (VEC && whole && t0 + kSteps <= len) {
+      const long long first = chunk_at(r);
+      char* bx = reinterpret_cast<char*>(dx + b * d.dx_sb + c0 + first * d.dx_st);
+      char* bg = reinterpret_cast<char*>(dgate + b * d.dgate_sb + c0 + first * d.dgate_st);
+      const uint32_t sx = (uint32_t)d.dx_st * (uint32_t)sizeof(T), sg = (uint32_t)d.dgate_st * (uint32_t)sizeof(T);
+      uint32_t ox = (w * kSteps + kSteps - 1) * sx + lane * 2 * (uint32_t)sizeof(T);
+      uint32_t og = (w * kSteps + kSteps - 1) * sg + lane * 2 * (uint32_t)sizeof(T);
 #pragma unroll
-      for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
+      for (int i = kSteps - 1; i >= 0; --i, ox -= sx, og -= sg) {
         const uint64_t g = f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk));
         q = f2_mul(a[i], g);
-        if (live) {
-          store_pair<T, VEC>(px, f2_open(f2_mul(s[i], g)), two);
-          store_pair<T, VEC>(pg, f2_open(f2_mul(f2_mul(q, s[i]), past[i])), two);
-        }
+        store_at<T>(bx, ox, f2_mul(s[i], g));
+        store_at<T>(bg, og, f2_mul(f2_mul(q, s[i]), past[i]));
       }
     } else {
+      T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
+      T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
 #pragma unroll
       for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
         const uint64_t g = f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk));
@@ -512,7 +533,7 @@ int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... ar
   return FRNNT_OK;
 }
 
-// Rows of 16-byte vectors throughout.
+// Rows of 16-byte vectors throughout, and chunks that 32-bit offsets span.
 bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void*> ptrs,
                 std::initializer_list<long long> strides) {
   if (d.D % 2) return false;
@@ -520,6 +541,8 @@ bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void
     if (!aligned(p, 16)) return false;
   for (long long v : strides)
     if (v * size_of(d.dtype) % 16) return false;
+  for (long long st : {d.x_st, d.gate_st, d.h_st, d.dh_st, d.dx_st, d.dgate_st})
+    if (st > (1LL << 31) / kChunk / 4) return false;
   return true;
 }
 
