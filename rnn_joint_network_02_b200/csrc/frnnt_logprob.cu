@@ -143,168 +143,238 @@ struct FwdParams {
   int32_t *top_ids, *status;
 };
 
-// The share of one warp (number g of G that share the row, 2 KB each in turn):
-// statistics and alternatives in one pass over the vectors.
-template <typename T, bool TOP>
-__device__ __forceinline__ void scan_row(const Row<T>& row, int g, int G, int lane, int top, Stats& st, Best& best) {
-  constexpr int E = Row<T>::E;
-  for (int base = g * 32 * kVecs; base < row.nvec; base += G * 32 * kVecs) {
-    float z[kVecs][E], vmax[kVecs];
-    const int n = min(kVecs, (row.nvec - base + 31) / 32);
-    uint4 raw[kVecs];
+// What a lane holds of a row: kVecs vectors, from vector `base` on, 32 apart.
+struct Chunk {
+  uint4 v[kVecs];
+};
+template <typename T>
+__device__ __forceinline__ void load_chunk(Chunk& c, const Row<T>& row, int base, int lane) {
+  const uint4* q = row.vec(base + lane);
+  if (base + 32 * kVecs <= row.nvec) {
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int v = base + u * 32 + lane;
-      const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
-      raw[u] = make_uint4(none, none, none, none);
-      if (v < row.nvec) raw[u] = __ldg(row.vec(v));
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      vmax[u] = -INFINITY;
-      if (u < n) {
-        unpack<T>(raw[u], z[u]);
-#pragma unroll
-        for (int i = 0; i < E; i += 2) vmax[u] = fmaxf(vmax[u], fmaxf(z[u][i], z[u][i + 1]));
-      }
-      m = fmaxf(m, vmax[u]);
-    }
-    const float ref = fmaxf(m, st.m);
-    if (ref > st.m) rescale(st, ref);
-    // a lane that has seen only -inf (or NaN) sums about 0
-    const float at = ref == -INFINITY ? 0.f : -ref;
-    const uint64_t at2 = f2_of(at, at), l2e = f2_of(kLog2e, kLog2e);
-    uint64_t s2 = f2_of(0.f, 0.f), w2 = s2;
+    for (int u = 0; u < kVecs; ++u) c.v[u] = __ldg(q + 32 * u);
+  } else {
+    const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
-      if (u < n) {
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const float2 d = f2_open(f2_mul(f2_add(f2_of(z[u][i], z[u][i + 1]), at2), l2e));
-          const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
-          const uint64_t e2 = f2_of(exp2_approx(d0), exp2_approx(d1));
-          s2 = f2_add(s2, e2);
-          w2 = f2_fma(e2, f2_of(d0, d1), w2);
-        }
-      }
-    const float2 s = f2_open(s2), w = f2_open(w2);
-    st.s += s.x + s.y;
-    st.w += w.x + w.y;
+      c.v[u] = base + u * 32 + lane < row.nvec ? __ldg(q + 32 * u) : make_uint4(none, none, none, none);
+  }
+}
 
-    if constexpr (TOP) {
-      float bound = best.bound;
-      if (bound == -INFINITY) {
-        // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
-        uint32_t k = order_key(m), kth = 0;
-        for (int i = 0; i < top; ++i) {
-          kth = __reduce_max_sync(kAll, k);
-          if (k == kth) k = 0;
-        }
-        if (kth) bound = key_value(kth);
-      }
-      unsigned vecs = 0;
+// The largest of a vector's elements (a NaN counts as none).
+template <typename T>
+__device__ __forceinline__ float vector_max(uint4 r) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  } else {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(r.x), "r"(r.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(r.z), "r"(r.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    const float lo = __uint_as_float(a << 16), hi = __uint_as_float(a & 0xFFFF0000u);
+    return fmaxf(lo, fmaxf(hi, -INFINITY));
+  }
+}
+
+// The first n of a chunk's vectors: statistics and alternatives.  The maxima
+// are taken on the packed elements, which are unpacked once, vector by vector.
+template <typename T, bool TOP, bool WHOLE>
+__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, const Row<T>& row, int base, int lane, int top,
+                                           Stats& st, Best& best) {
+  constexpr int E = Row<T>::E;
+  float vmax[kVecs], m = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-        if (base + u * 32 + lane < row.nvec && vmax[u] >= bound) vecs |= 1u << u;
-      if (__any_sync(kAll, vecs)) {
-        while (__any_sync(kAll, vecs)) {
-          // the lane's next vector that may hold candidates, read again (from cache) to be indexed
-          unsigned elems = 0;
-          int col = 0;
-          uint4 r = make_uint4(0, 0, 0, 0);
-          if (vecs) {
-            const int v = base + (__ffs(vecs) - 1) * 32 + lane;
-            vecs &= vecs - 1;
-            r = __ldg(row.vec(v));
-            col = row.head + v * E;
-            float f[E];
-            unpack<T>(r, f);
+  for (int u = 0; u < kVecs; ++u) {
+    vmax[u] = WHOLE || u < n ? vector_max<T>(c.v[u]) : -INFINITY;
+    m = fmaxf(m, vmax[u]);
+  }
+  const float ref = fmaxf(m, st.m);
+  if (ref > st.m) rescale(st, ref);
+  // a lane that has seen only -inf (or NaN) sums about 0
+  const float at = ref == -INFINITY ? 0.f : -ref;
+  const uint64_t at2 = f2_of(at, at), l2e = f2_of(kLog2e, kLog2e);
+  uint64_t s2 = f2_of(0.f, 0.f), w2 = s2;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-              if (!(f[i] < bound)) elems |= 1u << i;
-          }
-          while (__any_sync(kAll, elems)) {
-            uint64_t c = 0;
-            if (elems) {
-              const int i = __ffs(elems) - 1;
-              elems &= elems - 1;
-              const int word = sizeof(T) == 4 ? i : i >> 1;
-              uint32_t x = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
-              if (sizeof(T) == 2) x = (i & 1) ? x & 0xFFFF0000u : x << 16;
-              c = candidate(__uint_as_float(x), col + i);
-            }
-            best.offer(c, lane, top);
-          }
-        }
-        best.settle(top);
+  for (int u = 0; u < kVecs; ++u)
+    if (WHOLE || u < n) {
+      float z[E];
+      unpack<T>(c.v[u], z);
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const float2 d = f2_open(f2_mul(f2_add(f2_of(z[i], z[i + 1]), at2), l2e));
+        const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
+        const uint64_t e2 = f2_of(exp2_approx(d0), exp2_approx(d1));
+        s2 = f2_add(s2, e2);
+        w2 = f2_fma(e2, f2_of(d0, d1), w2);
       }
     }
-  }
-  if (g == 0 && row.head + row.tail > 0) {
-    const int col = row.edge(lane);
-    const float z = col >= 0 ? to_f32<T>(__ldg(row.p + col)) : -INFINITY;
-    const float ref = fmaxf(z, st.m);
-    if (ref > st.m) rescale(st, ref);
-    const float d = at_least((z + (ref == -INFINITY ? 0.f : -ref)) * kLog2e, kFloor), e = exp2_approx(d);
-    st.s += e;
-    st.w = fmaf(e, d, st.w);
-    if constexpr (TOP) best.offer(col >= 0 ? candidate(z, col) : 0, lane, top);
+  const float2 s = f2_open(s2), w = f2_open(w2);
+  st.s += s.x + s.y;
+  st.w += w.x + w.y;
+
+  if constexpr (TOP) {
+    float bound = best.bound;
+    if (bound == -INFINITY) {
+      // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
+      uint32_t k = order_key(m), kth = 0;
+      for (int i = 0; i < top; ++i) {
+        kth = __reduce_max_sync(kAll, k);
+        if (k == kth) k = 0;
+      }
+      if (kth) bound = key_value(kth);
+    }
+    unsigned vecs = 0;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (vmax[u] >= bound && (WHOLE || base + u * 32 + lane < row.nvec)) vecs |= 1u << u;
+    if (__any_sync(kAll, vecs)) {
+      while (__any_sync(kAll, vecs)) {
+        // the lane's next vector that may hold candidates, read again (from cache) to be indexed
+        unsigned elems = 0;
+        int col = 0;
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (vecs) {
+          const int v = base + (__ffs(vecs) - 1) * 32 + lane;
+          vecs &= vecs - 1;
+          r = __ldg(row.vec(v));
+          col = row.head + v * E;
+          float f[E];
+          unpack<T>(r, f);
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (!(f[i] < bound)) elems |= 1u << i;
+        }
+        while (__any_sync(kAll, elems)) {
+          uint64_t x = 0;
+          if (elems) {
+            const int i = __ffs(elems) - 1;
+            elems &= elems - 1;
+            const int word = sizeof(T) == 4 ? i : i >> 1;
+            uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
+            if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
+            x = candidate(__uint_as_float(y), col + i);
+          }
+          best.offer(x, lane, top);
+        }
+      }
+      best.settle(top);
+    }
   }
 }
-
-// What one warp writes for a row from its joined statistics and alternatives.
 template <typename T, bool TOP>
-__device__ __forceinline__ void write_row(const FwdParams& p, long long n, int lane, const Stats& st, const Best& best,
-                                          int token, float zt) {
-  const bool empty = st.s == 0.f;
-  const float ls = logf(st.s);
-  if (lane == 0) {
-    p.lse[n] = empty ? -INFINITY : st.m + ls;
-    p.entropy[n] = empty ? 0.f : fmaf(st.w / st.s, -kLn2, ls);
-  }
-  if (lane < p.K) {
-    const bool given = token >= 0 && token < p.V;
-    if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
-    p.logp[n * p.K + lane] = !given ? 0.f : empty ? -INFINITY : (zt - st.m) - ls;
-  }
-  if (TOP && lane < p.top) {
-    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best.mine;
-    p.top_logp[n * p.top + lane] = empty ? -INFINITY : (key_value((uint32_t)(best.mine >> 32)) - st.m) - ls;
-  }
+__device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, int lane, int top, Stats& st,
+                                     Best& best) {
+  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, TOP, true>(c, kVecs, row, base, lane, top, st, best);
+  else scan_chunk<T, TOP, false>(c, (row.nvec - base + 31) / 32, row, base, lane, top, st, best);
 }
 
+// Head and tail: one element a lane (-inf where there is none).
 template <typename T>
-__device__ __forceinline__ void read_token(const FwdParams& p, long long n, const T* row, int lane, int& token, float& zt) {
-  token = FRNNT_NO_TOKEN;
-  zt = 0.f;
-  if (lane < p.K) {
-    token = p.tokens[n * p.K + lane];
-    if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row + token));
+__device__ __forceinline__ float load_edge(const Row<T>& row, int lane) {
+  const int col = row.edge(lane);
+  return col >= 0 ? to_f32<T>(__ldg(row.p + col)) : -INFINITY;
+}
+template <typename T, bool TOP>
+__device__ __forceinline__ void scan_edge(float z, const Row<T>& row, int lane, int top, Stats& st, Best& best) {
+  const float ref = fmaxf(z, st.m);
+  if (ref > st.m) rescale(st, ref);
+  const float d = at_least((z + (ref == -INFINITY ? 0.f : -ref)) * kLog2e, kFloor), e = exp2_approx(d);
+  st.s += e;
+  st.w = fmaf(e, d, st.w);
+  if constexpr (TOP) {
+    const int col = row.edge(lane);
+    best.offer(col >= 0 ? candidate(z, col) : 0, lane, top);
   }
 }
 
-// A warp a row.
+// A row's values from its joined statistics; ls = ln st.s.  st.s is 0 where
+// nothing but -inf was seen.
+__device__ __forceinline__ void write_stats(const FwdParams& p, long long n, const Stats& st, float ls) {
+  const bool empty = st.s == 0.f;
+  p.lse[n] = empty ? -INFINITY : st.m + ls;
+  p.entropy[n] = empty ? 0.f : fmaf(st.w / st.s, -kLn2, ls);
+}
+__device__ __forceinline__ void write_token(const FwdParams& p, long long n, int k, const Stats& st, float ls, int token,
+                                            float z) {
+  const bool given = token >= 0 && token < p.V;
+  if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
+  p.logp[n * p.K + k] = !given ? 0.f : st.s == 0.f ? -INFINITY : (z - st.m) - ls;
+}
+__device__ __forceinline__ void write_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
+                                          const Best& best) {
+  if (lane < p.top) {
+    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best.mine;
+    p.top_logp[n * p.top + lane] =
+        st.s == 0.f ? -INFINITY : (key_value((uint32_t)(best.mine >> 32)) - st.m) - ls;
+  }
+}
+
+// A warp takes `rows` rows, one after another, with the next one's vectors on
+// their way.  Lane i keeps row i's joined statistics, so that the logarithms,
+// divisions and stores of up to 32 rows are made at once, a lane a row; the
+// values of their first tokens are fetched before the rows are scanned.
+constexpr int kEarly = 2;
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kWarps * 32) logprob_warp_kernel(FwdParams p, const T* __restrict__ logits) {
+__global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
   const int lane = threadIdx.x & 31;
-  const long long n = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= p.N) return;
-  const Row<T> row(logits + n * p.ld, p.V);
-  int token;
-  float zt;
-  read_token<T>(p, n, row.p, lane, token, zt);
-  Stats st{-INFINITY, 0.f, 0.f};
-  Best best;
-  scan_row<T, TOP>(row, 0, 1, lane, p.top, st, best);
-  join_warp(st);
-  write_row<T, TOP>(p, n, lane, st, best, token, zt);
+  const long long n0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
+  if (n0 >= p.N) return;
+  const int count = (int)min((long long)rows, p.N - n0);
+  Chunk next;
+  Row<T> row(logits + n0 * p.ld, p.V);
+  load_chunk(next, row, 0, lane);
+  float edge = row.head + row.tail ? load_edge(row, lane) : 0.f;
+
+  const long long mine = n0 + lane;   // the row that this lane finishes
+  const bool have = lane < count;
+  int token[kEarly];
+  float zt[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) token[k] = have && k < p.K ? p.tokens[mine * p.K + k] : FRNNT_NO_TOKEN;
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    zt[k] = token[k] >= 0 && token[k] < p.V ? to_f32<T>(__ldg(logits + mine * p.ld + token[k])) : 0.f;
+
+  Stats kept{0.f, 0.f, 0.f};
+  for (int i = 0; i < count; ++i) {
+    Stats st{-INFINITY, 0.f, 0.f};
+    Best best;
+    const Row<T> here = row;
+    const float z = edge;
+    if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
+    for (int base = 0;; base += 32 * kVecs) {
+      const Chunk c = next;
+      const bool last = base + 32 * kVecs >= here.nvec;
+      if (!last) {
+        load_chunk(next, here, base + 32 * kVecs, lane);
+      } else if (i + 1 < count) {
+        load_chunk(next, row, 0, lane);
+        if (row.head + row.tail) edge = load_edge(row, lane);
+      }
+      if (here.nvec) scan<T, TOP>(c, here, base, lane, p.top, st, best);
+      if (last) break;
+    }
+    if (here.head + here.tail) scan_edge<T, TOP>(z, here, lane, p.top, st, best);
+    join_warp(st);
+    if (lane == i) kept = st;
+    if constexpr (TOP) write_top(p, n0 + i, lane, st, logf(st.s), best);
+  }
+  if (!have) return;
+  const float ls = logf(kept.s);
+  write_stats(p, mine, kept, ls);
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (k < p.K) write_token(p, mine, k, kept, ls, token[k], zt[k]);
+  for (int k = kEarly; k < p.K; ++k) {
+    const int t = p.tokens[mine * p.K + k];
+    write_token(p, mine, k, kept, ls, t, t >= 0 && t < p.V ? to_f32<T>(__ldg(logits + mine * p.ld + t)) : 0.f);
+  }
 }
 
 // A cluster of CL blocks a row: the warps' statistics and alternatives meet in
 // the shared memory of the first block.
 template <typename T, bool TOP, int CL>
-__global__ void __launch_bounds__(kWarps * 32) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
+__global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
   __shared__ Stats stats[kWarps * CL];
   __shared__ uint64_t lists[TOP ? kWarps * CL : 1][FRNNT_MAX_TOP];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -312,12 +382,25 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_block_kernel(FwdParams p,
   const long long n = blockIdx.x / CL;
   if (CL > 1) cluster_arrive();
   const Row<T> row(logits + n * p.ld, p.V);
+  constexpr int kStride = kWarps * CL * 32 * kVecs;
+  Chunk next;
+  int base = g * 32 * kVecs;
+  if (base < row.nvec) load_chunk(next, row, base, lane);
   int token = FRNNT_NO_TOKEN;
-  float zt = 0.f;
-  if (g == 0) read_token<T>(p, n, row.p, lane, token, zt);
+  float zt = 0.f, edge = 0.f;
+  if (g == 0) {
+    if (row.head + row.tail) edge = load_edge(row, lane);
+    if (lane < p.K) token = p.tokens[n * p.K + lane];
+    if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row.p + token));
+  }
   Stats st{-INFINITY, 0.f, 0.f};
   Best best;
-  scan_row<T, TOP>(row, g, kWarps * CL, lane, p.top, st, best);
+  for (; base < row.nvec; base += kStride) {
+    const Chunk c = next;
+    if (base + kStride < row.nvec) load_chunk(next, row, base + kStride, lane);
+    scan<T, TOP>(c, row, base, lane, p.top, st, best);
+  }
+  if (g == 0 && row.head + row.tail) scan_edge<T, TOP>(edge, row, lane, p.top, st, best);
   join_warp(st);
   if (CL > 1) {
     cluster_wait();   // the first block runs: its shared memory may be written
@@ -343,7 +426,10 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_block_kernel(FwdParams p,
   join_warp(st);
   if constexpr (TOP)
     for (int k = 1; k < kWarps * CL; ++k) best.offer(lane < p.top ? lists[k][lane] : 0, lane, p.top);
-  write_row<T, TOP>(p, n, lane, st, best, token, zt);
+  const float ls = logf(st.s);
+  if (lane == 0) write_stats(p, n, st, ls);
+  if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
+  if constexpr (TOP) write_top(p, n, lane, st, ls, best);
 }
 
 // ------------------------------------------------------------------ backward
@@ -381,8 +467,8 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)]
   }
 }
 
-// dz_j = -p_j (A + B log2 p_j) with A = sum of the coefficients + dentropy
-// entropy and B = dentropy ln2, plus the coefficients of column j: the dense
+// dz_j = p_j (A + B log2 p_j) with -A = sum of the coefficients + dentropy
+// entropy and -B = dentropy ln2, plus the coefficients of column j: the dense
 // part first, then the few columns that have coefficients are written again
 // by the lanes that hold them.  Every element is read before it is written,
 // by the same warp, so dlogits may be the logits' memory (no non-coherent loads).
@@ -431,51 +517,62 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   }
   // a row without any term, or with nothing left by its mask, gets zeros
   const bool none = l == -INFINITY || (!p.dentropy && !__any_sync(kAll, id[0] >= 0 || id[1] >= 0));
-  const float A = fmaf(de, h, sum), B = de * kLn2;
+  const float A = -fmaf(de, h, sum), B = -de * kLn2;
   auto dense = [&](float z) {
     const float d = at_least((z - l) * kLog2e, kFloor);
-    return -exp2_approx(d) * fmaf(B, d, A);
+    return exp2_approx(d) * fmaf(B, d, A);
   };
   auto patch = [&](int lo, int hi) {   // columns lo .. hi - 1 have been written by this warp
     __syncwarp();
-    if (!none) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(dense(zt[i]) + total[i]);
-    }
+    for (int i = 0; i < 2; ++i)
+      if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(dense(zt[i]) + total[i]);
   };
 
   const bool whole = ((uintptr_t)(out + row.head) & 15u) == 0;
+  T* const body = out + row.head;
+  if (none) {
+    float zero[E] = {};
+    for (int v = v0 + lane; v < v1; v += 32) store_vec<T>(body + (long long)v * E, zero, whole);
+    if (seg == 0 && row.edge(lane) >= 0) out[row.edge(lane)] = from_f32<T>(0.f);
+    return;
+  }
   const uint64_t l2 = f2_of(-l, -l), l2e = f2_of(kLog2e, kLog2e), A2 = f2_of(A, A), B2 = f2_of(B, B);
-  for (int base = v0; base < v1; base += 32 * kVecs) {
-    uint4 raw[kVecs];
+  auto vector = [&](uint4 raw, T* to) {
+    float f[E];
+    unpack<T>(raw, f);
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int v = base + u * 32 + lane;
-      if (v < v1) raw[u] = *row.vec(v);
+    for (int i = 0; i < E; i += 2) {
+      const float2 d = f2_open(f2_mul(f2_add(f2_of(f[i], f[i + 1]), l2), l2e));
+      const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
+      const float2 g = f2_open(f2_mul(f2_of(exp2_approx(d0), exp2_approx(d1)), f2_fma(B2, f2_of(d0, d1), A2)));
+      f[i] = g.x;
+      f[i + 1] = g.y;
     }
+    store_vec<T>(to, f, whole);
+  };
+  for (int base = v0; base < v1; base += 32 * kVecs) {
+    const uint4* src = row.vec(base + lane);
+    T* to = body + (long long)(base + lane) * E;
+    uint4 raw[kVecs];
+    if (base + 32 * kVecs <= v1) {
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int v = base + u * 32 + lane;
-      if (v < v1) {
-        float f[E];
-        unpack<T>(raw[u], f);
+      for (int u = 0; u < kVecs; ++u) raw[u] = src[32 * u];
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const float2 d = f2_open(f2_mul(f2_add(f2_of(f[i], f[i + 1]), l2), l2e));
-          const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
-          const float2 g = f2_open(f2_mul(f2_of(-exp2_approx(d0), -exp2_approx(d1)), f2_fma(B2, f2_of(d0, d1), A2)));
-          f[i] = none ? 0.f : g.x;
-          f[i + 1] = none ? 0.f : g.y;
-        }
-        store_vec<T>(out + row.head + v * E, f, whole);
-      }
+      for (int u = 0; u < kVecs; ++u) vector(raw[u], to + 32 * u * E);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (base + u * 32 + lane < v1) raw[u] = src[32 * u];
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (base + u * 32 + lane < v1) vector(raw[u], to + 32 * u * E);
     }
     patch(row.head + base * E, row.head + min(v1, base + 32 * kVecs) * E);
   }
   if (seg == 0 && row.head + row.tail > 0) {
     const int col = row.edge(lane);
-    if (col >= 0) out[col] = from_f32<T>(none ? 0.f : dense(to_f32<T>(row.p[col])));
+    if (col >= 0) out[col] = from_f32<T>(dense(to_f32<T>(row.p[col])));
     patch(0, row.head);
     patch(row.head + row.nvec * E, p.V);
   }
@@ -487,7 +584,12 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
   if (chunks <= 2 || (chunks <= 4 && p.N >= 148 * 32)) {
-    launch_k(logprob_warp_kernel<T, TOP>, dim3((p.N + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, logits);
+    // as many rows a warp as spread the rows over the resident warps (3 blocks an SM)
+    int rows = (p.N + 148 * 3 * kWarps - 1) / (148 * 3 * kWarps);
+    if (rows > 32) rows = 32;
+    const int warps = (p.N + rows - 1) / rows;
+    launch_k(logprob_warp_kernel<T, TOP>, dim3((warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, rows,
+             logits);
   } else {
     int cl = 1;
     while (cl < 8 && (long long)p.N * cl < 148 && chunks > (long long)kWarps * cl) cl *= 2;
