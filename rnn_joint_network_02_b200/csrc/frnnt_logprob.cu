@@ -112,25 +112,59 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 __device__ __forceinline__ uint64_t candidate(float v, int col) { return ((uint64_t)order_key(v) << 32) | (uint32_t)~col; }
 
-// A warp's best `top` so far, in descending order, one a lane.
+// Descending order across the lanes (bitonic): merges of 2, 4, ... 32 sorted runs.
+__device__ __forceinline__ uint64_t exchange(uint64_t x, int lane, int apart, bool keep_larger) {
+  const uint64_t y = __shfl_xor_sync(kAll, x, apart);
+  return (x > y) == keep_larger ? x : y;
+}
+__device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
+#pragma unroll
+  for (int run = 2; run <= 32; run *= 2)
+#pragma unroll
+    for (int apart = run / 2; apart > 0; apart /= 2)
+      x = exchange(x, lane, apart, ((lane & apart) == 0) == ((lane & run) == 0 || run == 32));
+  return x;
+}
+// The 32 largest of two descending lists, descending.
+__device__ __forceinline__ uint64_t merge_desc(uint64_t x, uint64_t y, int lane) {
+  const uint64_t r = __shfl_xor_sync(kAll, y, 31);   // reversed: the maxima form a bitonic sequence
+  x = x > r ? x : r;
+#pragma unroll
+  for (int apart = 16; apart > 0; apart /= 2) x = exchange(x, lane, apart, (lane & apart) == 0);
+  return x;
+}
+
+// A warp's best so far: a descending list, one entry a lane, and candidates
+// that wait in shared memory until there are enough to be sorted and merged.
+constexpr int kWaiting = 64;
 struct Best {
-  uint64_t mine = 0;       // this lane's entry
-  float bound = -INFINITY; // the last entry's value once there are `top`: smaller values are no candidates
-  // Takes the candidates of the lanes that offer one (0: none), one after another.
-  __device__ __forceinline__ void offer(uint64_t c, int lane, int top) {
-    unsigned from = __ballot_sync(kAll, c > __shfl_sync(kAll, mine, top - 1));
-    while (from) {
-      const int src = __ffs(from) - 1;
-      from &= from - 1;
-      const uint64_t x = __shfl_sync(kAll, c, src);
-      const int pos = __popc(__ballot_sync(kAll, mine > x));
-      const uint64_t up = __shfl_up_sync(kAll, mine, 1);
-      if (lane >= pos) mine = lane == pos ? x : up;
-    }
+  uint64_t mine = 0;        // this lane's entry of the list
+  float bound = -INFINITY;  // the top-th entry's value once there is one: smaller values are no candidates
+  uint64_t last = 0;        // that entry, or 0
+  int waiting = 0;
+  uint64_t* buffer;         // kWaiting places of the warp's own
+
+  __device__ __forceinline__ void flush(int lane, int top) {   // up to 32 of those that wait
+    __syncwarp();
+    const uint64_t x = lane < waiting ? buffer[lane] : 0;
+    const uint64_t rest = lane + 32 < waiting ? buffer[lane + 32] : 0;
+    __syncwarp();
+    if (lane + 32 < waiting) buffer[lane] = rest;
+    waiting = max(0, waiting - 32);
+    const uint64_t y = sort_desc(x, lane);
+    mine = merge_desc(mine, y, lane);
+    last = __shfl_sync(kAll, mine, top - 1);
+    bound = last >> 32 == 0 ? -INFINITY : key_value((uint32_t)(last >> 32));
   }
-  __device__ __forceinline__ void settle(int top) {
-    const uint32_t k = (uint32_t)(__shfl_sync(kAll, mine, top - 1) >> 32);
-    bound = k == 0u ? -INFINITY : key_value(k);
+  // Puts down one candidate of each lane that has one (at most 32 may wait before).
+  __device__ __forceinline__ void offer(bool has, uint64_t x, int lane) {
+    has = has && x > last;
+    const unsigned from = __ballot_sync(kAll, has);
+    if (has) buffer[waiting + __popc(from & ((1u << lane) - 1))] = x;
+    waiting += __popc(from);
+  }
+  __device__ __forceinline__ void finish(int lane, int top) {
+    while (waiting) flush(lane, top);
   }
 };
 
@@ -176,13 +210,12 @@ __device__ __forceinline__ float vector_max(uint4 r) {
   }
 }
 
-// The first n of a chunk's vectors: statistics and alternatives.  The maxima
+// The statistics of the first n of a chunk's vectors, and their maxima, which
 // are taken on the packed elements, which are unpacked once, vector by vector.
-template <typename T, bool TOP, bool WHOLE>
-__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, const Row<T>& row, int base, int lane, int top,
-                                           Stats& st, Best& best) {
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st, float (&vmax)[kVecs]) {
   constexpr int E = Row<T>::E;
-  float vmax[kVecs], m = -INFINITY;
+  float m = -INFINITY;
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     vmax[u] = WHOLE || u < n ? vector_max<T>(c.v[u]) : -INFINITY;
@@ -212,60 +245,62 @@ __device__ __forceinline__ void scan_chunk(const Chunk& c, int n, const Row<T>& 
   st.s += s.x + s.y;
   st.w += w.x + w.y;
 
-  if constexpr (TOP) {
-    float bound = best.bound;
-    if (bound == -INFINITY) {
-      // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
-      uint32_t k = order_key(m), kth = 0;
-      for (int i = 0; i < top; ++i) {
-        kth = __reduce_max_sync(kAll, k);
-        if (k == kth) k = 0;
-      }
-      if (kth) bound = key_value(kth);
+}
+
+// The candidates of a chunk whose vectors' maxima are vmax.
+template <typename T>
+__device__ __forceinline__ void collect(const float (&vmax)[kVecs], const Row<T>& row, int base, int lane, int top,
+                                        Best& best) {
+  constexpr int E = Row<T>::E;
+  float bound = best.bound;
+  if (bound == -INFINITY) {
+    // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
+    uint32_t k = order_key(fmaxf(fmaxf(vmax[0], vmax[1]), fmaxf(vmax[2], vmax[3]))), kth = 0;
+    for (int i = 0; i < top; ++i) {
+      kth = __reduce_max_sync(kAll, k);
+      if (k == kth) k = 0;
     }
-    unsigned vecs = 0;
+    if (kth) bound = key_value(kth);
+  }
+  unsigned vecs = 0, elems = 0;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (vmax[u] >= bound && (WHOLE || base + u * 32 + lane < row.nvec)) vecs |= 1u << u;
-    if (__any_sync(kAll, vecs)) {
-      while (__any_sync(kAll, vecs)) {
+  for (int u = 0; u < kVecs; ++u)
+    if (vmax[u] >= bound && base + u * 32 + lane < row.nvec) vecs |= 1u << u;
+  uint4 r = make_uint4(0, 0, 0, 0);
+  int col = 0;
+  for (;;) {
+    const bool left = __any_sync(kAll, vecs | elems);
+    if (left) {
+      if (!elems && vecs) {
         // the lane's next vector that may hold candidates, read again (from cache) to be indexed
-        unsigned elems = 0;
-        int col = 0;
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (vecs) {
-          const int v = base + (__ffs(vecs) - 1) * 32 + lane;
-          vecs &= vecs - 1;
-          r = __ldg(row.vec(v));
-          col = row.head + v * E;
-          float f[E];
-          unpack<T>(r, f);
+        const int v = base + (__ffs(vecs) - 1) * 32 + lane;
+        vecs &= vecs - 1;
+        r = __ldg(row.vec(v));
+        col = row.head + v * E;
+        float f[E];
+        unpack<T>(r, f);
 #pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (!(f[i] < bound)) elems |= 1u << i;
-        }
-        while (__any_sync(kAll, elems)) {
-          uint64_t x = 0;
-          if (elems) {
-            const int i = __ffs(elems) - 1;
-            elems &= elems - 1;
-            const int word = sizeof(T) == 4 ? i : i >> 1;
-            uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
-            if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
-            x = candidate(__uint_as_float(y), col + i);
-          }
-          best.offer(x, lane, top);
-        }
+        for (int i = 0; i < E; ++i)
+          if (!(f[i] < bound)) elems |= 1u << i;
       }
-      best.settle(top);
+      const int i = elems ? __ffs(elems) - 1 : 0;
+      const int word = sizeof(T) == 4 ? i : i >> 1;
+      uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
+      if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
+      best.offer(elems != 0, candidate(__uint_as_float(y), col + i), lane);
+      elems &= elems - 1;
     }
+    if (best.waiting > kWaiting - 32 || (!left && best.waiting && best.bound == -INFINITY)) best.flush(lane, top);
+    else if (!left) break;
   }
 }
 template <typename T, bool TOP>
 __device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, int lane, int top, Stats& st,
                                      Best& best) {
-  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, TOP, true>(c, kVecs, row, base, lane, top, st, best);
-  else scan_chunk<T, TOP, false>(c, (row.nvec - base + 31) / 32, row, base, lane, top, st, best);
+  float vmax[kVecs];
+  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, true>(c, kVecs, st, vmax);
+  else scan_chunk<T, false>(c, (row.nvec - base + 31) / 32, st, vmax);
+  if constexpr (TOP) collect(vmax, row, base, lane, top, best);
 }
 
 // Head and tail: one element a lane (-inf where there is none).
@@ -283,7 +318,7 @@ __device__ __forceinline__ void scan_edge(float z, const Row<T>& row, int lane, 
   st.w = fmaf(e, d, st.w);
   if constexpr (TOP) {
     const int col = row.edge(lane);
-    best.offer(col >= 0 ? candidate(z, col) : 0, lane, top);
+    best.offer(col >= 0 && !(z < best.bound), candidate(z, col), lane);
   }
 }
 
@@ -301,11 +336,10 @@ __device__ __forceinline__ void write_token(const FwdParams& p, long long n, int
   p.logp[n * p.K + k] = !given ? 0.f : st.s == 0.f ? -INFINITY : (z - st.m) - ls;
 }
 __device__ __forceinline__ void write_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
-                                          const Best& best) {
+                                          uint64_t best) {
   if (lane < p.top) {
-    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best.mine;
-    p.top_logp[n * p.top + lane] =
-        st.s == 0.f ? -INFINITY : (key_value((uint32_t)(best.mine >> 32)) - st.m) - ls;
+    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best;
+    p.top_logp[n * p.top + lane] = st.s == 0.f ? -INFINITY : (key_value((uint32_t)(best >> 32)) - st.m) - ls;
   }
 }
 
@@ -316,6 +350,7 @@ __device__ __forceinline__ void write_top(const FwdParams& p, long long n, int l
 constexpr int kEarly = 2;
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
+  __shared__ uint64_t waiting[TOP ? kWarps : 1][kWaiting];
   const int lane = threadIdx.x & 31;
   const long long n0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
   if (n0 >= p.N) return;
@@ -339,6 +374,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   for (int i = 0; i < count; ++i) {
     Stats st{-INFINITY, 0.f, 0.f};
     Best best;
+    best.buffer = waiting[TOP ? threadIdx.x >> 5 : 0];
     const Row<T> here = row;
     const float z = edge;
     if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
@@ -357,7 +393,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
     if (here.head + here.tail) scan_edge<T, TOP>(z, here, lane, p.top, st, best);
     join_warp(st);
     if (lane == i) kept = st;
-    if constexpr (TOP) write_top(p, n0 + i, lane, st, logf(st.s), best);
+    if constexpr (TOP) {
+      best.finish(lane, p.top);
+      write_top(p, n0 + i, lane, st, logf(st.s), best.mine);
+    }
   }
   if (!have) return;
   const float ls = logf(kept.s);
@@ -371,65 +410,102 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   }
 }
 
-// A cluster of CL blocks a row: the warps' statistics and alternatives meet in
-// the shared memory of the first block.
+// The sorted lists of a block's (or cluster's) `n` warps, in shared memory, become
+// one, in lists[0]: pairs in parallel, a warp a pair.  All warps call it.
+__device__ __forceinline__ void merge_lists(uint64_t (*lists)[FRNNT_MAX_TOP], int n, int w, int lane) {
+  for (int half = n / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (w < half) lists[w][lane] = merge_desc(lists[w][lane], lists[w + half][lane], lane);
+  }
+  __syncthreads();
+}
+
+// A cluster of CL blocks a row.  One block: it takes rows in turn, with the
+// next row's vectors on their way.  The warps' statistics meet in shared
+// memory (two places, so that one barrier a row is enough) and one of them,
+// another each row, finishes the row.
 template <typename T, bool TOP, int CL>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
-  __shared__ Stats stats[kWarps * CL];
-  __shared__ uint64_t lists[TOP ? kWarps * CL : 1][FRNNT_MAX_TOP];
+  __shared__ Stats stats[2][kWarps * CL];
+  __shared__ uint64_t lists[TOP ? kWarps : 1][FRNNT_MAX_TOP];
+  __shared__ uint64_t tops[TOP ? CL : 1][FRNNT_MAX_TOP];
+  __shared__ uint64_t waiting[TOP ? kWarps : 1][kWaiting];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
-  const long long n = blockIdx.x / CL;
-  if (CL > 1) cluster_arrive();
-  const Row<T> row(logits + n * p.ld, p.V);
   constexpr int kStride = kWarps * CL * 32 * kVecs;
+  if (CL > 1) cluster_arrive();
+  const long long step = CL > 1 ? p.N : gridDim.x;   // a cluster takes one row
+  long long n = blockIdx.x / CL;
   Chunk next;
-  int base = g * 32 * kVecs;
-  if (base < row.nvec) load_chunk(next, row, base, lane);
-  int token = FRNNT_NO_TOKEN;
-  float zt = 0.f, edge = 0.f;
-  if (g == 0) {
-    if (row.head + row.tail) edge = load_edge(row, lane);
-    if (lane < p.K) token = p.tokens[n * p.K + lane];
-    if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row.p + token));
-  }
-  Stats st{-INFINITY, 0.f, 0.f};
-  Best best;
-  for (; base < row.nvec; base += kStride) {
-    const Chunk c = next;
-    if (base + kStride < row.nvec) load_chunk(next, row, base + kStride, lane);
-    scan<T, TOP>(c, row, base, lane, p.top, st, best);
-  }
-  if (g == 0 && row.head + row.tail) scan_edge<T, TOP>(edge, row, lane, p.top, st, best);
-  join_warp(st);
-  if (CL > 1) {
-    cluster_wait();   // the first block runs: its shared memory may be written
-    if (lane == 0) {
-      const uint32_t at = in_cluster(&stats[g], 0);
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(st.m) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(st.s) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(st.w) : "memory");
+  Row<T> row(logits + n * p.ld, p.V);
+  if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
+  float edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : 0.f;
+  for (int i = 0; n < p.N; ++i, n += step) {
+    const int writer = CL > 1 ? 0 : i % kWarps;
+    int token = FRNNT_NO_TOKEN;
+    float zt = 0.f;
+    if (g == writer) {
+      if (lane < p.K) token = p.tokens[n * p.K + lane];
+      if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row.p + token));
     }
-    if (TOP && lane < p.top)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&lists[g][lane], 0)), "l"(best.mine) : "memory");
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    if (lane == 0) stats[g] = st;
-    if (TOP && lane < p.top) lists[g][lane] = best.mine;
-    __syncthreads();
-  }
-  if (g != 0) return;
-  st = lane < kWarps * CL ? stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+    Stats st{-INFINITY, 0.f, 0.f};
+    Best best;
+    best.buffer = waiting[TOP ? w : 0];
+    const Row<T> here = row;
+    const float z = edge;
+    const bool more = n + step < p.N;
+    if (more) row = Row<T>(logits + (n + step) * p.ld, p.V);
+    int base = g * 32 * kVecs;
+    for (;; base += kStride) {
+      const Chunk c = next;
+      if (base + kStride < here.nvec) {
+        load_chunk(next, here, base + kStride, lane);
+      } else if (more) {
+        if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
+        if (g == 0 && row.head + row.tail) edge = load_edge(row, lane);
+      }
+      if (base < here.nvec) scan<T, TOP>(c, here, base, lane, p.top, st, best);
+      if (base + kStride >= here.nvec) break;
+    }
+    if (g == 0 && here.head + here.tail) scan_edge<T, TOP>(z, here, lane, p.top, st, best);
+    join_warp(st);
+    Stats* meet = stats[i & 1];
+    if constexpr (TOP) {
+      best.finish(lane, p.top);
+      lists[w][lane] = best.mine;
+      merge_lists(lists, kWarps, w, lane);
+    }
+    if (CL > 1) {
+      cluster_wait();   // the first block runs: its shared memory may be written
+      if (lane == 0) {
+        const uint32_t at = in_cluster(&meet[g], 0);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(st.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(st.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(st.w) : "memory");
+      }
+      if (TOP && w == 0)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&tops[rank][lane], 0)), "l"(lists[0][lane])
+                     : "memory");
+      cluster_arrive();
+      cluster_wait();
+      if (rank != 0) return;
+      if constexpr (TOP) merge_lists(tops, CL, w, lane);
+    } else {
+      if (lane == 0) meet[g] = st;
+      if (TOP && w == 0) tops[0][lane] = lists[0][lane];
+      __syncthreads();
+    }
+    if (w == writer) {
+      st = lane < kWarps * CL ? meet[lane] : Stats{-INFINITY, 0.f, 0.f};
 #pragma unroll
-  for (int k = 32; k < kWarps * CL; k += 32) join(st, stats[k + lane]);
-  join_warp(st);
-  if constexpr (TOP)
-    for (int k = 1; k < kWarps * CL; ++k) best.offer(lane < p.top ? lists[k][lane] : 0, lane, p.top);
-  const float ls = logf(st.s);
-  if (lane == 0) write_stats(p, n, st, ls);
-  if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
-  if constexpr (TOP) write_top(p, n, lane, st, ls, best);
+      for (int k = 32; k < kWarps * CL; k += 32) join(st, meet[k + lane]);
+      join_warp(st);
+      const float ls = logf(st.s);
+      if (lane == 0) write_stats(p, n, st, ls);
+      if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
+      if constexpr (TOP) write_top(p, n, lane, st, ls, tops[0][lane]);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ backward
@@ -583,9 +659,10 @@ template <typename T, bool TOP>
 void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
-  if (chunks <= 2 || (chunks <= 4 && p.N >= 148 * 32)) {
-    // as many rows a warp as spread the rows over the resident warps (3 blocks an SM)
-    int rows = (p.N + 148 * 3 * kWarps - 1) / (148 * 3 * kWarps);
+  constexpr int kBlocks = 148 * 3;                       // resident at a time
+  if (chunks <= 2) {
+    // as many rows a warp as spread them over the resident warps
+    int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
     if (rows > 32) rows = 32;
     const int warps = (p.N + rows - 1) / rows;
     launch_k(logprob_warp_kernel<T, TOP>, dim3((warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, rows,
@@ -593,7 +670,8 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   } else {
     int cl = 1;
     while (cl < 8 && (long long)p.N * cl < 148 && chunks > (long long)kWarps * cl) cl *= 2;
-    auto go = [&](auto kernel) { launch_k(kernel, dim3((unsigned)p.N * cl), dim3(kWarps * 32), 0, st, cl, p, logits); };
+    const int grid = cl > 1 ? p.N * cl : (p.N < kBlocks ? p.N : kBlocks);
+    auto go = [&](auto kernel) { launch_k(kernel, dim3(grid), dim3(kWarps * 32), 0, st, cl, p, logits); };
     if (cl == 1) go(logprob_block_kernel<T, TOP, 1>);
     else if (cl == 2) go(logprob_block_kernel<T, TOP, 2>);
     else if (cl == 4) go(logprob_block_kernel<T, TOP, 4>);
