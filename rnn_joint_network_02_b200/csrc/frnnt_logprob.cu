@@ -134,39 +134,32 @@ __device__ __forceinline__ uint64_t merge_desc(uint64_t x, uint64_t y, int lane)
   return x;
 }
 
-// A warp's best so far: a descending list, one entry a lane, and candidates
-// that wait in shared memory until there are enough to be sorted and merged.
-constexpr int kWaiting = 64;
-struct Best {
-  uint64_t mine = 0;        // this lane's entry of the list
-  float bound = -INFINITY;  // the top-th entry's value once there is one: smaller values are no candidates
-  uint64_t last = 0;        // that entry, or 0
-  int waiting = 0;
-  uint64_t* buffer;         // kWaiting places of the warp's own
+// Candidates wait in shared memory, in any order, until they are sorted.
+constexpr int kWaiting = 256;
 
-  __device__ __forceinline__ void flush(int lane, int top) {   // up to 32 of those that wait
-    __syncwarp();
-    const uint64_t x = lane < waiting ? buffer[lane] : 0;
-    const uint64_t rest = lane + 32 < waiting ? buffer[lane + 32] : 0;
-    __syncwarp();
-    if (lane + 32 < waiting) buffer[lane] = rest;
-    waiting = max(0, waiting - 32);
-    const uint64_t y = sort_desc(x, lane);
-    mine = merge_desc(mine, y, lane);
-    last = __shfl_sync(kAll, mine, top - 1);
-    bound = last >> 32 == 0 ? -INFINITY : key_value((uint32_t)(last >> 32));
+// The 32 largest of n <= kWaiting candidates, descending, one a lane.
+__device__ __forceinline__ uint64_t sort_waiting(const uint64_t* buffer, int n, int lane) {
+  uint64_t best = 0;
+  for (int k = 0; k < n; k += 32) {
+    const uint64_t x = sort_desc(k + lane < n ? buffer[k + lane] : 0, lane);
+    best = k ? merge_desc(best, x, lane) : x;
   }
-  // Puts down one candidate of each lane that has one (at most 32 may wait before).
-  __device__ __forceinline__ void offer(bool has, uint64_t x, int lane) {
-    has = has && x > last;
-    const unsigned from = __ballot_sync(kAll, has);
-    if (has) buffer[waiting + __popc(from & ((1u << lane) - 1))] = x;
-    waiting += __popc(from);
+  return best;
+}
+
+// A value that at least `top` of the row's elements reach, from 32 lanes' maxima
+// of disjoint parts of it: the top-th largest of them.  -inf where there are
+// not as many above it.
+__device__ __forceinline__ float bound_of(float m, int top) {
+  uint32_t k = order_key(m), kth = 0;
+  for (int found = 0; found < top;) {
+    kth = __reduce_max_sync(kAll, k);
+    if (kth == 0) break;   // (a -inf has a key above 0)
+    found += __popc(__ballot_sync(kAll, k == kth));
+    if (k == kth) k = 0;
   }
-  __device__ __forceinline__ void finish(int lane, int top) {
-    while (waiting) flush(lane, top);
-  }
-};
+  return kth == 0 ? -INFINITY : key_value(kth);
+}
 
 // ------------------------------------------------------------------ forward
 struct FwdParams {
@@ -210,17 +203,15 @@ __device__ __forceinline__ float vector_max(uint4 r) {
   }
 }
 
-// The statistics of the first n of a chunk's vectors, and their maxima, which
-// are taken on the packed elements, which are unpacked once, vector by vector.
+// The statistics of the first n of a chunk's vectors.  The maximum is taken on
+// the packed elements, which are unpacked once, vector by vector.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st, float (&vmax)[kVecs]) {
+__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st) {
   constexpr int E = Row<T>::E;
   float m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    vmax[u] = WHOLE || u < n ? vector_max<T>(c.v[u]) : -INFINITY;
-    m = fmaxf(m, vmax[u]);
-  }
+  for (int u = 0; u < kVecs; ++u)
+    if (WHOLE || u < n) m = fmaxf(m, vector_max<T>(c.v[u]));
   const float ref = fmaxf(m, st.m);
   if (ref > st.m) rescale(st, ref);
   // a lane that has seen only -inf (or NaN) sums about 0
@@ -247,60 +238,10 @@ __device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st, flo
 
 }
 
-// The candidates of a chunk whose vectors' maxima are vmax.
 template <typename T>
-__device__ __forceinline__ void collect(const float (&vmax)[kVecs], const Row<T>& row, int base, int lane, int top,
-                                        Best& best) {
-  constexpr int E = Row<T>::E;
-  float bound = best.bound;
-  if (bound == -INFINITY) {
-    // no full list yet: the top-th largest of the 32 lanes' maxima bounds the answer from below
-    uint32_t k = order_key(fmaxf(fmaxf(vmax[0], vmax[1]), fmaxf(vmax[2], vmax[3]))), kth = 0;
-    for (int i = 0; i < top; ++i) {
-      kth = __reduce_max_sync(kAll, k);
-      if (k == kth) k = 0;
-    }
-    if (kth) bound = key_value(kth);
-  }
-  unsigned vecs = 0, elems = 0;
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u)
-    if (vmax[u] >= bound && base + u * 32 + lane < row.nvec) vecs |= 1u << u;
-  uint4 r = make_uint4(0, 0, 0, 0);
-  int col = 0;
-  for (;;) {
-    const bool left = __any_sync(kAll, vecs | elems);
-    if (left) {
-      if (!elems && vecs) {
-        // the lane's next vector that may hold candidates, read again (from cache) to be indexed
-        const int v = base + (__ffs(vecs) - 1) * 32 + lane;
-        vecs &= vecs - 1;
-        r = __ldg(row.vec(v));
-        col = row.head + v * E;
-        float f[E];
-        unpack<T>(r, f);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (!(f[i] < bound)) elems |= 1u << i;
-      }
-      const int i = elems ? __ffs(elems) - 1 : 0;
-      const int word = sizeof(T) == 4 ? i : i >> 1;
-      uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
-      if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
-      best.offer(elems != 0, candidate(__uint_as_float(y), col + i), lane);
-      elems &= elems - 1;
-    }
-    if (best.waiting > kWaiting - 32 || (!left && best.waiting && best.bound == -INFINITY)) best.flush(lane, top);
-    else if (!left) break;
-  }
-}
-template <typename T, bool TOP>
-__device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, int lane, int top, Stats& st,
-                                     Best& best) {
-  float vmax[kVecs];
-  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, true>(c, kVecs, st, vmax);
-  else scan_chunk<T, false>(c, (row.nvec - base + 31) / 32, st, vmax);
-  if constexpr (TOP) collect(vmax, row, base, lane, top, best);
+__device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, Stats& st) {
+  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, true>(c, kVecs, st);
+  else scan_chunk<T, false>(c, (row.nvec - base + 31) / 32, st);
 }
 
 // Head and tail: one element a lane (-inf where there is none).
@@ -309,17 +250,66 @@ __device__ __forceinline__ float load_edge(const Row<T>& row, int lane) {
   const int col = row.edge(lane);
   return col >= 0 ? to_f32<T>(__ldg(row.p + col)) : -INFINITY;
 }
-template <typename T, bool TOP>
-__device__ __forceinline__ void scan_edge(float z, const Row<T>& row, int lane, int top, Stats& st, Best& best) {
+__device__ __forceinline__ void scan_edge(float z, Stats& st) {
   const float ref = fmaxf(z, st.m);
   if (ref > st.m) rescale(st, ref);
   const float d = at_least((z + (ref == -INFINITY ? 0.f : -ref)) * kLog2e, kFloor), e = exp2_approx(d);
   st.s += e;
   st.w = fmaf(e, d, st.w);
-  if constexpr (TOP) {
-    const int col = row.edge(lane);
-    best.offer(col >= 0 && !(z < best.bound), candidate(z, col), lane);
+}
+
+// ---- best alternatives of a row
+// The scan leaves every lane with the largest of its own elements, so a bound
+// on the top-th value costs a few reductions, and only the lanes that hold one
+// of the best read their elements again (from cache).  With random rows 32
+// ln(32 / (32 - top)) elements reach the bound: 9 for the best 8, 31 for 20.
+// `put` takes a candidate.
+template <typename T, typename Put>
+__device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lane, float bound, float edge, Put put) {
+  constexpr int E = Row<T>::E;
+  for (int base = g * 32 * kVecs + lane; base < row.nvec; base += G * 32 * kVecs) {
+    uint4 r[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (base + 32 * u < row.nvec) r[u] = __ldg(row.vec(base + 32 * u));
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (base + 32 * u < row.nvec && vector_max<T>(r[u]) >= bound) {
+        float z[E];
+        unpack<T>(r[u], z);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (z[i] >= bound) put(candidate(z[i], row.head + (base + 32 * u) * E + i));
+      }
   }
+  if (g == 0 && edge >= bound && row.edge(lane) >= 0) put(candidate(edge, row.edge(lane)));
+}
+
+// Rows that the bound does not thin out (many equal values, or fewer than `top`
+// elements above -inf): one warp goes through the row in order, with the list
+// of the best so far, which stops later columns of equal value.  Descending,
+// one a lane; `buffer`: 64 places.
+template <typename T>
+__device__ __noinline__ uint64_t best_in_order(const T* p, int V, int top, uint64_t* buffer) {
+  const int lane = threadIdx.x & 31;
+  uint64_t best = 0, last = 0;
+  int waiting = 0;
+  for (int j = 0; j < V || waiting; j += 32) {
+    const uint64_t x = j + lane < V ? candidate(to_f32<T>(__ldg(p + j + lane)), j + lane) : 0;
+    const unsigned from = __ballot_sync(kAll, x > last);
+    if (x > last) buffer[waiting + __popc(from & ((1u << lane) - 1))] = x;
+    waiting += __popc(from);
+    if (waiting > 32 || (waiting && j + 32 >= V)) {
+      __syncwarp();
+      best = merge_desc(best, sort_desc(lane < waiting ? buffer[lane] : 0, lane), lane);
+      const uint64_t rest = lane + 32 < waiting ? buffer[lane + 32] : 0;
+      __syncwarp();
+      if (lane + 32 < waiting) buffer[lane] = rest;
+      waiting = max(0, waiting - 32);
+      last = __shfl_sync(kAll, best, top - 1);
+    }
+  }
+  return best;
 }
 
 // A row's values from its joined statistics; ls = ln st.s.  st.s is 0 where
@@ -350,15 +340,16 @@ __device__ __forceinline__ void write_top(const FwdParams& p, long long n, int l
 constexpr int kEarly = 2;
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
-  __shared__ uint64_t waiting[TOP ? kWarps : 1][kWaiting];
-  const int lane = threadIdx.x & 31;
-  const long long n0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
+  __shared__ uint64_t buffers[TOP ? kWarps : 1][kWaiting];
+  __shared__ int counts[kWarps];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long n0 = ((long long)blockIdx.x * kWarps + w) * rows;
   if (n0 >= p.N) return;
   const int count = (int)min((long long)rows, p.N - n0);
   Chunk next;
   Row<T> row(logits + n0 * p.ld, p.V);
   load_chunk(next, row, 0, lane);
-  float edge = row.head + row.tail ? load_edge(row, lane) : 0.f;
+  float edge = row.head + row.tail ? load_edge(row, lane) : -INFINITY;
 
   const long long mine = n0 + lane;   // the row that this lane finishes
   const bool have = lane < count;
@@ -373,8 +364,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   Stats kept{0.f, 0.f, 0.f};
   for (int i = 0; i < count; ++i) {
     Stats st{-INFINITY, 0.f, 0.f};
-    Best best;
-    best.buffer = waiting[TOP ? threadIdx.x >> 5 : 0];
     const Row<T> here = row;
     const float z = edge;
     if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
@@ -385,17 +374,30 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
         load_chunk(next, here, base + 32 * kVecs, lane);
       } else if (i + 1 < count) {
         load_chunk(next, row, 0, lane);
-        if (row.head + row.tail) edge = load_edge(row, lane);
+        edge = row.head + row.tail ? load_edge(row, lane) : -INFINITY;
       }
-      if (here.nvec) scan<T, TOP>(c, here, base, lane, p.top, st, best);
+      if (here.nvec) scan<T>(c, here, base, st);
       if (last) break;
     }
-    if (here.head + here.tail) scan_edge<T, TOP>(z, here, lane, p.top, st, best);
+    if (here.head + here.tail) scan_edge(z, st);
+    const float most = st.m;   // of this lane's elements
     join_warp(st);
     if (lane == i) kept = st;
     if constexpr (TOP) {
-      best.finish(lane, p.top);
-      write_top(p, n0 + i, lane, st, logf(st.s), best.mine);
+      const float bound = bound_of(most, p.top);
+      if (lane == 0) counts[w] = 0;
+      __syncwarp();
+      if (bound > -INFINITY && most >= bound)
+        collect(here, 0, 1, lane, bound, z, [&](uint64_t x) {
+          const int at = atomicAdd(&counts[w], 1);
+          if (at < kWaiting) buffers[w][at] = x;
+        });
+      __syncwarp();
+      const int found = counts[w];
+      const uint64_t best = bound > -INFINITY && found <= kWaiting ? sort_waiting(buffers[w], found, lane)
+                                                                   : best_in_order(here.p, p.V, p.top, buffers[w]);
+      write_top(p, n0 + i, lane, st, logf(st.s), best);
+      __syncwarp();
     }
   }
   if (!have) return;
@@ -410,37 +412,36 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   }
 }
 
-// The sorted lists of a block's (or cluster's) `n` warps, in shared memory, become
-// one, in lists[0]: pairs in parallel, a warp a pair.  All warps call it.
-__device__ __forceinline__ void merge_lists(uint64_t (*lists)[FRNNT_MAX_TOP], int n, int w, int lane) {
-  for (int half = n / 2; half > 0; half /= 2) {
-    __syncthreads();
-    if (w < half) lists[w][lane] = merge_desc(lists[w][lane], lists[w + half][lane], lane);
-  }
-  __syncthreads();
-}
-
 // A cluster of CL blocks a row.  One block: it takes rows in turn, with the
-// next row's vectors on their way.  The warps' statistics meet in shared
-// memory (two places, so that one barrier a row is enough) and one of them,
-// another each row, finishes the row.
+// next row's vectors on their way.  The warps' statistics (and the maxima of the
+// lanes, over the warps) meet in shared memory, in every block of a cluster;
+// one warp, another each row, finishes the row.  What meets has two places, so
+// that the next row's can be put down while this one's are read.
+template <int CL>
+struct Meeting {
+  Stats stats[kWarps * CL];
+  float most[kWarps * CL][32];
+  uint64_t buffer[kWaiting];
+  int count;
+};
 template <typename T, bool TOP, int CL>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
-  __shared__ Stats stats[2][kWarps * CL];
-  __shared__ uint64_t lists[TOP ? kWarps : 1][FRNNT_MAX_TOP];
-  __shared__ uint64_t tops[TOP ? CL : 1][FRNNT_MAX_TOP];
-  __shared__ uint64_t waiting[TOP ? kWarps : 1][kWaiting];
+  __shared__ Meeting<CL> meetings[CL > 1 ? 1 : 2];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
-  constexpr int kStride = kWarps * CL * 32 * kVecs;
+  constexpr int kShare = kWarps * CL, kStride = kShare * 32 * kVecs;
   if (CL > 1) cluster_arrive();
   const long long step = CL > 1 ? p.N : gridDim.x;   // a cluster takes one row
   long long n = blockIdx.x / CL;
   Chunk next;
   Row<T> row(logits + n * p.ld, p.V);
   if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
-  float edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : 0.f;
+  float edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : -INFINITY;
+  if (threadIdx.x == 0)
+    for (Meeting<CL>& m : meetings) m.count = 0;
+  __syncthreads();
   for (int i = 0; n < p.N; ++i, n += step) {
+    Meeting<CL>& meet = meetings[CL > 1 ? 0 : i & 1];
     const int writer = CL > 1 ? 0 : i % kWarps;
     int token = FRNNT_NO_TOKEN;
     float zt = 0.f;
@@ -449,61 +450,88 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams
       if (token >= 0 && token < p.V) zt = to_f32<T>(__ldg(row.p + token));
     }
     Stats st{-INFINITY, 0.f, 0.f};
-    Best best;
-    best.buffer = waiting[TOP ? w : 0];
     const Row<T> here = row;
     const float z = edge;
     const bool more = n + step < p.N;
     if (more) row = Row<T>(logits + (n + step) * p.ld, p.V);
-    int base = g * 32 * kVecs;
-    for (;; base += kStride) {
+    for (int base = g * 32 * kVecs;; base += kStride) {
       const Chunk c = next;
       if (base + kStride < here.nvec) {
         load_chunk(next, here, base + kStride, lane);
       } else if (more) {
         if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
-        if (g == 0 && row.head + row.tail) edge = load_edge(row, lane);
+        edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : -INFINITY;
       }
-      if (base < here.nvec) scan<T, TOP>(c, here, base, lane, p.top, st, best);
+      if (base < here.nvec) scan<T>(c, here, base, st);
       if (base + kStride >= here.nvec) break;
     }
-    if (g == 0 && here.head + here.tail) scan_edge<T, TOP>(z, here, lane, p.top, st, best);
+    if (g == 0 && here.head + here.tail) scan_edge(z, st);
+    const float most = st.m;   // of this lane's elements
     join_warp(st);
-    Stats* meet = stats[i & 1];
-    if constexpr (TOP) {
-      best.finish(lane, p.top);
-      lists[w][lane] = best.mine;
-      merge_lists(lists, kWarps, w, lane);
-    }
     if (CL > 1) {
-      cluster_wait();   // the first block runs: its shared memory may be written
-      if (lane == 0) {
-        const uint32_t at = in_cluster(&meet[g], 0);
+      cluster_wait();   // all blocks run: their shared memory may be written
+      if (lane < (TOP ? CL : 1)) {
+        const uint32_t at = in_cluster(&meet.stats[g], lane);
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(st.m) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(st.s) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(st.w) : "memory");
       }
-      if (TOP && w == 0)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&tops[rank][lane], 0)), "l"(lists[0][lane])
-                     : "memory");
+      if constexpr (TOP)
+        for (int k = 0; k < CL; ++k)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cluster(&meet.most[g][lane], k)), "f"(most) : "memory");
       cluster_arrive();
       cluster_wait();
-      if (rank != 0) return;
-      if constexpr (TOP) merge_lists(tops, CL, w, lane);
+      if (!TOP && rank != 0) return;
     } else {
-      if (lane == 0) meet[g] = st;
-      if (TOP && w == 0) tops[0][lane] = lists[0][lane];
+      if (lane == 0) meet.stats[g] = st;
+      if constexpr (TOP) meet.most[g][lane] = most;
       __syncthreads();
     }
+    float bound = -INFINITY;
+    if constexpr (TOP) {
+      float m = -INFINITY;
+#pragma unroll 8
+      for (int k = 0; k < kShare; ++k) m = fmaxf(m, meet.most[k][lane]);
+      bound = bound_of(m, p.top);
+      if (bound > -INFINITY && most >= bound)
+        collect(here, g, kShare, lane, bound, z, [&](uint64_t x) {
+          if constexpr (CL > 1) {
+            uint32_t at;
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
+                         : "=r"(at)
+                         : "r"(in_cluster(&meet.count, 0))
+                         : "memory");
+            if (at < kWaiting)
+              asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&meet.buffer[at], 0)), "l"(x) : "memory");
+          } else {
+            const int at = atomicAdd(&meet.count, 1);
+            if (at < kWaiting) meet.buffer[at] = x;
+          }
+        });
+      if (CL > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+      } else {
+        __syncthreads();
+      }
+    }
     if (w == writer) {
-      st = lane < kWarps * CL ? meet[lane] : Stats{-INFINITY, 0.f, 0.f};
+      st = lane < kShare ? meet.stats[lane] : Stats{-INFINITY, 0.f, 0.f};
 #pragma unroll
-      for (int k = 32; k < kWarps * CL; k += 32) join(st, meet[k + lane]);
+      for (int k = 32; k < kShare; k += 32) join(st, meet.stats[k + lane]);
       join_warp(st);
       const float ls = logf(st.s);
       if (lane == 0) write_stats(p, n, st, ls);
       if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
-      if constexpr (TOP) write_top(p, n, lane, st, ls, tops[0][lane]);
+      if constexpr (TOP) {
+        const int found = meet.count;
+        write_top(p, n, lane, st, ls,
+                  bound > -INFINITY && found <= kWaiting ? sort_waiting(meet.buffer, found, lane)
+                                                         : best_in_order(here.p, p.V, p.top, meet.buffer));
+        __syncwarp();
+        if (lane == 0) meet.count = 0;
+      }
     }
   }
 }
@@ -660,7 +688,7 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
   constexpr int kBlocks = 148 * 3;                       // resident at a time
-  if (chunks <= 2) {
+  if (chunks <= 2 || (chunks < kWarps && p.N >= 148 * kWarps)) {
     // as many rows a warp as spread them over the resident warps
     int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
     if (rows > 32) rows = 32;
