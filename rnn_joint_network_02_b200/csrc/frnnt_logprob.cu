@@ -260,27 +260,41 @@ __device__ __forceinline__ void scan_edge(float z, Stats& st) {
 
 // ---- best alternatives of a row
 // The scan leaves every lane with the largest of its own elements, so a bound
-// on the top-th value costs a few reductions, and only the lanes that hold one
-// of the best read their elements again (from cache).  With random rows 32
-// ln(32 / (32 - top)) elements reach the bound: 9 for the best 8, 31 for 20.
-// `put` takes a candidate.
+// on the top-th value costs a few reductions, and only what the lanes hold
+// whose largest reaches it is read again (from cache): 32 vectors at a time,
+// one a lane, whichever lane had them.  With random rows 32 ln(32 / (32 - top))
+// elements reach the bound: 9 for the best 8, 31 for 20.  `put` takes a
+// candidate; `who`: 32 places of the warp's own.
 template <typename T, typename Put>
-__device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lane, float bound, float edge, Put put) {
+__device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lane, float most, float bound, float edge,
+                                        uint8_t* who, Put put) {
   constexpr int E = Row<T>::E;
-  for (int base = g * 32 * kVecs + lane; base < row.nvec; base += G * 32 * kVecs) {
-    uint4 r[kVecs];
+  const unsigned from = __ballot_sync(kAll, most >= bound);
+  if (!from) return;
+  if (most >= bound) who[__popc(from & ((1u << lane) - 1))] = (uint8_t)lane;
+  __syncwarp();
+  const int span = 32 * kVecs, first = g * span;
+  const int each = max(0, (row.nvec - first + G * span - 1) / (G * span)) * kVecs;   // vectors of one lane
+  const int items = __popc(from) * each;
+  for (int t = lane; t < items; t += 32) {
+    const int owner = t / each, k = t - owner * each;
+    const int v = first + (k / kVecs) * (G * span) + (k % kVecs) * 32 + who[owner];
+    if (v >= row.nvec) continue;
+    const uint4 r = __ldg(row.vec(v));
+    if (!(vector_max<T>(r) >= bound)) continue;
+    float z[E];
+    unpack<T>(r, z);
+    unsigned elems = 0;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (base + 32 * u < row.nvec) r[u] = __ldg(row.vec(base + 32 * u));
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (base + 32 * u < row.nvec && vector_max<T>(r[u]) >= bound) {
-        float z[E];
-        unpack<T>(r[u], z);
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (z[i] >= bound) put(candidate(z[i], row.head + (base + 32 * u) * E + i));
-      }
+    for (int i = 0; i < E; ++i) elems |= (unsigned)(z[i] >= bound) << i;
+    while (elems) {
+      const int i = __ffs(elems) - 1;
+      elems &= elems - 1;
+      const int word = sizeof(T) == 4 ? i : i >> 1;
+      uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
+      if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
+      put(candidate(__uint_as_float(y), row.head + v * E + i));
+    }
   }
   if (g == 0 && edge >= bound && row.edge(lane) >= 0) put(candidate(edge, row.edge(lane)));
 }
@@ -325,11 +339,32 @@ __device__ __forceinline__ void write_token(const FwdParams& p, long long n, int
   if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
   p.logp[n * p.K + k] = !given ? 0.f : st.s == 0.f ? -INFINITY : (z - st.m) - ls;
 }
-__device__ __forceinline__ void write_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
-                                          uint64_t best) {
-  if (lane < p.top) {
-    p.top_ids[n * p.top + lane] = (int)~(uint32_t)best;
-    p.top_logp[n * p.top + lane] = st.s == 0.f ? -INFINITY : (key_value((uint32_t)(best >> 32)) - st.m) - ls;
+__device__ __forceinline__ void write_top(const FwdParams& p, long long n, int place, const Stats& st, float ls,
+                                          uint64_t x) {
+  if (place < p.top) {
+    p.top_ids[n * p.top + place] = (int)~(uint32_t)x;
+    p.top_logp[n * p.top + place] = st.s == 0.f ? -INFINITY : (key_value((uint32_t)(x >> 32)) - st.m) - ls;
+  }
+}
+// The row's alternatives from its candidates.  Few: each finds its place by
+// counting the larger ones; more: sorted; too many, or no bound: the row in order.
+template <typename T>
+__device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
+                                           const T* row, float bound, int found, uint64_t* buffer) {
+  if (bound > -INFINITY && found <= 64) {
+    const uint64_t x = lane < found ? buffer[lane] : 0, y = lane + 32 < found ? buffer[lane + 32] : 0;
+    int px = 0, py = 0;
+    for (int k = 0; k < found; ++k) {
+      const uint64_t o = buffer[k];
+      px += o > x;
+      py += o > y;
+    }
+    if (lane < found) write_top(p, n, px, st, ls, x);
+    if (lane + 32 < found) write_top(p, n, py, st, ls, y);
+  } else {
+    write_top(p, n, lane, st, ls,
+              bound > -INFINITY && found <= kWaiting ? sort_waiting(buffer, found, lane)
+                                                     : best_in_order(row, p.V, p.top, buffer));
   }
 }
 
@@ -342,6 +377,7 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
   __shared__ uint64_t buffers[TOP ? kWarps : 1][kWaiting];
   __shared__ int counts[kWarps];
+  __shared__ uint8_t who[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long n0 = ((long long)blockIdx.x * kWarps + w) * rows;
   if (n0 >= p.N) return;
@@ -387,16 +423,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
       const float bound = bound_of(most, p.top);
       if (lane == 0) counts[w] = 0;
       __syncwarp();
-      if (bound > -INFINITY && most >= bound)
-        collect(here, 0, 1, lane, bound, z, [&](uint64_t x) {
+      if (bound > -INFINITY)
+        collect(here, 0, 1, lane, most, bound, z, who[w], [&](uint64_t x) {
           const int at = atomicAdd(&counts[w], 1);
           if (at < kWaiting) buffers[w][at] = x;
         });
       __syncwarp();
-      const int found = counts[w];
-      const uint64_t best = bound > -INFINITY && found <= kWaiting ? sort_waiting(buffers[w], found, lane)
-                                                                   : best_in_order(here.p, p.V, p.top, buffers[w]);
-      write_top(p, n0 + i, lane, st, logf(st.s), best);
+      finish_top(p, n0 + i, lane, st, logf(st.s), here.p, bound, counts[w], buffers[w]);
       __syncwarp();
     }
   }
@@ -427,6 +460,7 @@ struct Meeting {
 template <typename T, bool TOP, int CL>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
   __shared__ Meeting<CL> meetings[CL > 1 ? 1 : 2];
+  __shared__ uint8_t who[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
   constexpr int kShare = kWarps * CL, kStride = kShare * 32 * kVecs;
@@ -493,8 +527,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams
 #pragma unroll 8
       for (int k = 0; k < kShare; ++k) m = fmaxf(m, meet.most[k][lane]);
       bound = bound_of(m, p.top);
-      if (bound > -INFINITY && most >= bound)
-        collect(here, g, kShare, lane, bound, z, [&](uint64_t x) {
+      if (bound > -INFINITY)
+        collect(here, g, kShare, lane, most, bound, z, who[w], [&](uint64_t x) {
           if constexpr (CL > 1) {
             uint32_t at;
             asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
@@ -525,10 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams
       if (lane == 0) write_stats(p, n, st, ls);
       if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
       if constexpr (TOP) {
-        const int found = meet.count;
-        write_top(p, n, lane, st, ls,
-                  bound > -INFINITY && found <= kWaiting ? sort_waiting(meet.buffer, found, lane)
-                                                         : best_in_order(here.p, p.V, p.top, meet.buffer));
+        finish_top(p, n, lane, st, ls, here.p, bound, meet.count, meet.buffer);
         __syncwarp();
         if (lane == 0) meet.count = 0;
       }
