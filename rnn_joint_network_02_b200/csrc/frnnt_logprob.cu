@@ -148,17 +148,20 @@ __device__ __forceinline__ uint64_t sort_waiting(const uint64_t* buffer, int n, 
 }
 
 // A value that at least `top` of the row's elements reach, from 32 lanes' maxima
-// of disjoint parts of it: the top-th largest of them.  -inf where there are
-// not as many above it.
-__device__ __forceinline__ float bound_of(float m, int top) {
-  uint32_t k = order_key(m), kth = 0;
-  for (int found = 0; found < top;) {
-    kth = __reduce_max_sync(kAll, k);
-    if (kth == 0) break;   // (a -inf has a key above 0)
-    found += __popc(__ballot_sync(kAll, k == kth));
-    if (k == kth) k = 0;
+// of disjoint parts of it: the top-th largest of them, -inf where fewer are
+// above it.  Each lane counts the larger ones (in shared memory: `all`, 32
+// places of the warp's own).
+__device__ __forceinline__ float bound_of(float m, int lane, int top, float* all) {
+  all[lane] = m;
+  __syncwarp();
+  int larger = 0;
+#pragma unroll
+  for (int k = 0; k < 32; k += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(all + k);
+    larger += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
   }
-  return kth == 0 ? -INFINITY : key_value(kth);
+  const uint32_t kth = __reduce_min_sync(kAll, larger < top ? order_key(m) : 0xFFFFFFFFu);
+  return key_value(kth);
 }
 
 // ------------------------------------------------------------------ forward
@@ -274,11 +277,11 @@ __device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lan
   if (most >= bound) who[__popc(from & ((1u << lane) - 1))] = (uint8_t)lane;
   __syncwarp();
   const int span = 32 * kVecs, first = g * span;
-  const int each = max(0, (row.nvec - first + G * span - 1) / (G * span)) * kVecs;   // vectors of one lane
-  const int items = __popc(from) * each;
+  const int chunks = max(0, (row.nvec - first + G * span - 1) / (G * span));   // of the warp
+  const int items = __popc(from) * chunks * kVecs;
   for (int t = lane; t < items; t += 32) {
-    const int owner = t / each, k = t - owner * each;
-    const int v = first + (k / kVecs) * (G * span) + (k % kVecs) * 32 + who[owner];
+    const int q = t / kVecs, owner = chunks == 1 ? q : q / chunks;
+    const int v = first + (q - owner * chunks) * (G * span) + (t % kVecs) * 32 + who[owner];
     if (v >= row.nvec) continue;
     const uint4 r = __ldg(row.vec(v));
     if (!(vector_max<T>(r) >= bound)) continue;
@@ -352,15 +355,12 @@ template <typename T>
 __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
                                            const T* row, float bound, int found, uint64_t* buffer) {
   if (bound > -INFINITY && found <= 64) {
-    const uint64_t x = lane < found ? buffer[lane] : 0, y = lane + 32 < found ? buffer[lane + 32] : 0;
-    int px = 0, py = 0;
-    for (int k = 0; k < found; ++k) {
-      const uint64_t o = buffer[k];
-      px += o > x;
-      py += o > y;
+    for (int j = lane; j < found; j += 32) {
+      const uint64_t x = buffer[j];
+      int place = 0;
+      for (int k = 0; k < found; ++k) place += buffer[k] > x;
+      write_top(p, n, place, st, ls, x);
     }
-    if (lane < found) write_top(p, n, px, st, ls, x);
-    if (lane + 32 < found) write_top(p, n, py, st, ls, y);
   } else {
     write_top(p, n, lane, st, ls,
               bound > -INFINITY && found <= kWaiting ? sort_waiting(buffer, found, lane)
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   __shared__ uint64_t buffers[TOP ? kWarps : 1][kWaiting];
   __shared__ int counts[kWarps];
   __shared__ uint8_t who[kWarps][32];
+  __shared__ __align__(16) float maxima[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long n0 = ((long long)blockIdx.x * kWarps + w) * rows;
   if (n0 >= p.N) return;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
     join_warp(st);
     if (lane == i) kept = st;
     if constexpr (TOP) {
-      const float bound = bound_of(most, p.top);
+      const float bound = bound_of(most, lane, p.top, maxima[w]);
       if (lane == 0) counts[w] = 0;
       __syncwarp();
       if (bound > -INFINITY)
@@ -461,6 +462,7 @@ template <typename T, bool TOP, int CL>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
   __shared__ Meeting<CL> meetings[CL > 1 ? 1 : 2];
   __shared__ uint8_t who[kWarps][32];
+  __shared__ __align__(16) float maxima[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
   constexpr int kShare = kWarps * CL, kStride = kShare * 32 * kVecs;
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams
       float m = -INFINITY;
 #pragma unroll 8
       for (int k = 0; k < kShare; ++k) m = fmaxf(m, meet.most[k][lane]);
-      bound = bound_of(m, p.top);
+      bound = bound_of(m, lane, p.top, maxima[w]);
       if (bound > -INFINITY)
         collect(here, g, kShare, lane, most, bound, z, who[w], [&](uint64_t x) {
           if constexpr (CL > 1) {
