@@ -604,11 +604,148 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)]
   }
 }
 
-// dz_j = p_j (A + B log2 p_j) with -A = sum of the coefficients + dentropy
-// entropy and -B = dentropy ln2, plus the coefficients of column j: the dense
-// part first, then the few columns that have coefficients are written again
-// by the lanes that hold them.  Every element is read before it is written,
-// by the same warp, so dlogits may be the logits' memory (no non-coherent loads).
+// The gradient of a row: dz_j = p_j (A + B log2 p_j) with -A = sum of the
+// coefficients + dentropy entropy and -B = dentropy ln2, plus the coefficients
+// of column j.
+struct Slope {
+  float l, A, B;   // l: log-sum-exp
+  __device__ __forceinline__ float at(float z) const {
+    const float d = at_least((z - l) * kLog2e, kFloor);
+    return exp2_approx(d) * fmaf(B, d, A);
+  }
+  template <typename T>
+  __device__ __forceinline__ void vector(uint4 raw, T* to, bool whole) const {
+    constexpr int E = 16 / sizeof(T);
+    const uint64_t l2 = f2_of(-l, -l), l2e = f2_of(kLog2e, kLog2e), A2 = f2_of(A, A), B2 = f2_of(B, B);
+    float f[E];
+    unpack<T>(raw, f);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float2 d = f2_open(f2_mul(f2_add(f2_of(f[i], f[i + 1]), l2), l2e));
+      const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
+      const float2 g = f2_open(f2_mul(f2_of(exp2_approx(d0), exp2_approx(d1)), f2_fma(B2, f2_of(d0, d1), A2)));
+      f[i] = g.x;
+      f[i + 1] = g.y;
+    }
+    store_vec<T>(to, f, whole);
+  }
+  // kVecs vectors of a lane, 32 apart, those below n
+  template <typename T>
+  __device__ __forceinline__ void chunk(const uint4 (&raw)[kVecs], T* to, int n, bool whole) const {
+    if (n >= 32 * (kVecs - 1) + 1) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)), whole);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (32 * u < n) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)), whole);
+    }
+  }
+};
+// (plain loads: dlogits may be the logits' memory, and non-coherent ones are for memory that the kernel does not write)
+__device__ __forceinline__ void load_vecs(uint4 (&raw)[kVecs], const uint4* src, int n) {
+  if (n >= 32 * (kVecs - 1) + 1) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) raw[u] = src[32 * u];
+  } else {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (32 * u < n) raw[u] = src[32 * u];
+  }
+}
+
+// Short rows with few coefficients: a warp takes `rows` rows, one after another,
+// with the next one's vectors on their way.  Lane i prepares row i's slope
+// (the loads of up to 32 rows' scalars at once) and, when all rows are
+// written, writes the columns of its tokens again.  Every element is read
+// before it is written, by the same warp, so dlogits may be the logits' memory.
+constexpr int kSlots = 4;
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdParams p, int rows, const T* logits, T* dlogits) {
+  constexpr int E = Row<T>::E;
+  const int lane = threadIdx.x & 31;
+  const long long n0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
+  if (n0 >= p.N) return;
+  const int count = (int)min((long long)rows, p.N - n0);
+  Row<T> row(logits + n0 * p.ld, p.V);
+  uint4 next[kVecs];
+  load_vecs(next, row.vec(lane), row.nvec - lane);
+  float edge = row.edge(lane) >= 0 ? to_f32<T>(row.p[row.edge(lane)]) : 0.f;
+
+  const long long mine = n0 + lane;
+  const int nk = p.dlogp ? p.K : 0, slots = nk + (p.dtop ? p.top : 0);   // at most kSlots
+  int id[kSlots];
+  float coef[kSlots], zt[kSlots], sum = 0.f;
+  Slope own{-INFINITY, 0.f, 0.f};
+  if (lane < count) {
+    const float de = p.dentropy ? p.dentropy[mine] : 0.f, h = p.dentropy ? p.entropy[mine] : 0.f;
+    bool any = p.dentropy != nullptr;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      id[k] = -1;
+      coef[k] = zt[k] = 0.f;
+      if (k < slots) {
+        const int t = k < nk ? p.tokens[mine * p.K + k] : p.top_ids[mine * p.top + k - nk];
+        if (t >= 0 && t < p.V) {
+          id[k] = t;
+          coef[k] = k < nk ? p.dlogp[mine * p.K + k] : p.dtop[mine * p.top + k - nk];
+          zt[k] = to_f32<T>(logits[mine * p.ld + t]);
+          any = true;
+        } else if (!(k < nk && t == FRNNT_NO_TOKEN) && p.status) {
+          atomicOr(p.status, FRNNT_STATUS_LABEL);
+        }
+      }
+      sum += coef[k];
+    }
+    if (any) own = Slope{p.lse[mine], -fmaf(de, h, sum), -de * kLn2};
+  }
+  for (int i = 0; i < count; ++i) {
+    const Slope g{__shfl_sync(kAll, own.l, i), __shfl_sync(kAll, own.A, i), __shfl_sync(kAll, own.B, i)};
+    const Row<T> here = row;
+    T* const out = dlogits + (n0 + i) * p.ldd;
+    T* const body = out + here.head;
+    const bool whole = ((uintptr_t)body & 15u) == 0;
+    const float z = edge;
+    const int col = here.edge(lane);
+    if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
+    for (int base = lane;; base += 32 * kVecs) {
+      uint4 raw[kVecs];
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) raw[u] = next[u];
+      const bool last = base - lane + 32 * kVecs >= here.nvec;
+      if (!last) {
+        load_vecs(next, here.vec(base + 32 * kVecs), here.nvec - base - 32 * kVecs);
+      } else if (i + 1 < count) {
+        load_vecs(next, row.vec(lane), row.nvec - lane);
+        if (row.edge(lane) >= 0) edge = to_f32<T>(row.p[row.edge(lane)]);
+      }
+      T* to = body + (long long)base * E;
+      if (g.l != -INFINITY) {
+        g.chunk<T>(raw, to, here.nvec - base, whole);
+      } else {   // a row without any term, or with nothing left by its mask, gets zeros
+        const float zero[E] = {};
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+          if (base + 32 * u < here.nvec) store_vec<T>(to + 32 * u * E, zero, whole);
+      }
+      if (last) break;
+    }
+    if (col >= 0) out[col] = from_f32<T>(g.l == -INFINITY ? 0.f : g.at(z));
+  }
+  __syncwarp();   // the dense part of all rows is written
+  if (lane < count && own.l != -INFINITY) {
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      float total = 0.f;   // of all slots with the same column
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) total += id[j] == id[k] ? coef[j] : 0.f;
+      if (id[k] >= 0) dlogits[mine * p.ldd + id[k]] = from_f32<T>(own.at(zt[k]) + total);
+    }
+  }
+}
+
+// Any row: `segments` warps share it.  The columns with coefficients are written
+// again by the warp that wrote them, a lane two slots.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, const T* logits, T* dlogits) {
   constexpr int E = Row<T>::E;
@@ -654,16 +791,12 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   }
   // a row without any term, or with nothing left by its mask, gets zeros
   const bool none = l == -INFINITY || (!p.dentropy && !__any_sync(kAll, id[0] >= 0 || id[1] >= 0));
-  const float A = -fmaf(de, h, sum), B = -de * kLn2;
-  auto dense = [&](float z) {
-    const float d = at_least((z - l) * kLog2e, kFloor);
-    return exp2_approx(d) * fmaf(B, d, A);
-  };
+  const Slope g{l, -fmaf(de, h, sum), -de * kLn2};
   auto patch = [&](int lo, int hi) {   // columns lo .. hi - 1 have been written by this warp
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(dense(zt[i]) + total[i]);
+      if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(g.at(zt[i]) + total[i]);
   };
 
   const bool whole = ((uintptr_t)(out + row.head) & 15u) == 0;
@@ -674,53 +807,27 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
     if (seg == 0 && row.edge(lane) >= 0) out[row.edge(lane)] = from_f32<T>(0.f);
     return;
   }
-  const uint64_t l2 = f2_of(-l, -l), l2e = f2_of(kLog2e, kLog2e), A2 = f2_of(A, A), B2 = f2_of(B, B);
-  auto vector = [&](uint4 raw, T* to) {
-    float f[E];
-    unpack<T>(raw, f);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float2 d = f2_open(f2_mul(f2_add(f2_of(f[i], f[i + 1]), l2), l2e));
-      const float d0 = at_least(d.x, kFloor), d1 = at_least(d.y, kFloor);
-      const float2 g = f2_open(f2_mul(f2_of(exp2_approx(d0), exp2_approx(d1)), f2_fma(B2, f2_of(d0, d1), A2)));
-      f[i] = g.x;
-      f[i + 1] = g.y;
-    }
-    store_vec<T>(to, f, whole);
-  };
   for (int base = v0; base < v1; base += 32 * kVecs) {
-    const uint4* src = row.vec(base + lane);
-    T* to = body + (long long)(base + lane) * E;
     uint4 raw[kVecs];
-    if (base + 32 * kVecs <= v1) {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) raw[u] = src[32 * u];
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) vector(raw[u], to + 32 * u * E);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-        if (base + u * 32 + lane < v1) raw[u] = src[32 * u];
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-        if (base + u * 32 + lane < v1) vector(raw[u], to + 32 * u * E);
-    }
+    load_vecs(raw, row.vec(base + lane), v1 - base - lane);
+    g.chunk<T>(raw, body + (long long)(base + lane) * E, v1 - base - lane, whole);
     patch(row.head + base * E, row.head + min(v1, base + 32 * kVecs) * E);
   }
   if (seg == 0 && row.head + row.tail > 0) {
     const int col = row.edge(lane);
-    if (col >= 0) out[col] = from_f32<T>(dense(to_f32<T>(row.p[col])));
+    if (col >= 0) out[col] = from_f32<T>(g.at(to_f32<T>(row.p[col])));
     patch(0, row.head);
     patch(row.head + row.nvec * E, p.V);
   }
 }
 
 // ------------------------------------------------------------------ launches
+constexpr int kBlocks = 148 * 3;   // resident at a time
+
 template <typename T, bool TOP>
 void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
-  constexpr int kBlocks = 148 * 3;                       // resident at a time
   if (chunks <= 2 || (chunks < kWarps && p.N >= 148 * kWarps)) {
     // as many rows a warp as spread them over the resident warps
     int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
@@ -743,11 +850,20 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
 
 template <typename T>
 void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
-  p.segments = (p.V / (int)(16 / sizeof(T)) + kSegment - 1) / kSegment;
-  if (p.segments < 1) p.segments = 1;
-  const long long warps = (long long)p.N * p.segments;
-  launch_k(logprob_bwd_kernel<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, 1, p,
-           logits, dlogits);
+  const long long vecs = p.V / (long long)(16 / sizeof(T));
+  const int slots = (p.dlogp ? p.K : 0) + (p.dtop ? p.top : 0);
+  if (slots <= kSlots && vecs <= 2 * 32 * kVecs) {
+    int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
+    if (rows > 32) rows = 32;
+    const int warps = (p.N + rows - 1) / rows;
+    launch_k(logprob_bwd_rows_kernel<T>, dim3((warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, rows,
+             logits, dlogits);
+  } else {
+    p.segments = vecs <= kSegment ? 1 : (int)((vecs + kSegment - 1) / kSegment);
+    const long long warps = (long long)p.N * p.segments;
+    launch_k(logprob_bwd_kernel<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, 1, p,
+             logits, dlogits);
+  }
   note_launch();
 }
 
