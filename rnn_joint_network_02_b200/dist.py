@@ -141,7 +141,9 @@ def gpu_compute(mode: str = "tiled", durations=None, wgrad_f32: bool = True, **k
     ``durations``: the token-and-duration transducer, whose duration head
     W_d / b_d travels in the tensors dict like the other weights).  By default
     the weight gradients come back as the library's fp32 accumulators, views
-    of one flat buffer that the exchange reduces in place."""
+    of one flat buffer that the exchange reduces in place.  ``dropout``
+    (frnnt.Dropout) needs a seed of its own on each rank: its mask goes by an
+    entry's place in the rank's shard."""
     from . import frnnt
 
     def run(t, w):

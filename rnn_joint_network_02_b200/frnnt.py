@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -272,6 +273,7 @@ class Outputs:
             weights += [("dW_d", W_d), ("db_d", b_d)]
         self.dW_d = self.db_d = None
         self.wflat = None
+        self.dropped = None      # f and g after dropout, once a call with dropout has needed them
         if dims.wgrad_f32:
             # segments start on 16-byte boundaries (the library's alignment rule)
             sizes = [(t.numel() + 3) // 4 * 4 for _, t in weights]
@@ -294,19 +296,55 @@ class Outputs:
         return d
 
 
+class Dropout(NamedTuple):
+    """Dropout of a loss call's inputs f and g (the ``dropout`` argument of
+    fwd_bwd and its variants): each entry is dropped with probability p before
+    the joint network and the rest scaled by 1 / (1 - p), and df and dg are the
+    gradients for the f and g that were passed.  The mask comes from
+    ``dropout`` (below) and is never stored: f's entries take the counters from
+    ``offset`` on, g's those that follow.  A new call needs new numbers: another
+    ``seed``, or ``offset`` moved on by ``counters(f, g)``; ``seed`` may be a
+    device tensor (captured graphs).  Data-parallel ranks need a seed each."""
+    p: float
+    seed: "int | torch.Tensor"
+    offset: int = 0
+
+    @staticmethod
+    def counters(f, g) -> int:
+        """Counters that one call uses."""
+        return (f.numel() + 7) // 8 + (g.numel() + 7) // 8
+
+
+def _with_dropout(drop, f, g, out, stream, call):
+    """``call(f, g)`` on the dropped inputs, its df and dg masked alike."""
+    if out is not None and out.dropped is None:
+        out.dropped = (torch.empty_like(f), torch.empty_like(g))
+    fd, gd = (None, None) if out is None else out.dropped
+    at = (drop.offset, drop.offset + (f.numel() + 7) // 8)
+    loss, grads = call(dropout(f, drop.p, drop.seed, at[0], fd, stream), dropout(g, drop.p, drop.seed, at[1], gd, stream))
+    dropout(grads["df"], drop.p, drop.seed, at[0], grads["df"], stream)
+    dropout(grads["dg"], drop.p, drop.seed, at[1], grads["dg"], stream)
+    return loss, grads
+
+
 def fwd_bwd(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=None, mode="tiled", path="auto",
             chunk_cells=0, blank=0, out: Outputs | None = None, check=True, stream=None, loss="marginal",
-            wgrad_f32=False):
+            wgrad_f32=False, dropout: Dropout | None = None):
     """One call of frnnt_fwd_bwd on CUDA tensors.
 
     Float tensors are all float32 or all bfloat16; labels/T_len/U_len int32.
     ``loss`` is "marginal" (every alignment) or "viterbi" (the best one).
     ``wgrad_f32``: the weight gradients come back in fp32 (unrounded).
+    ``dropout``: of f and g, see Dropout.
     Returns (loss [B] fp32, dict of gradients).  With ``check`` the device
     status word is read back (one 4-byte device-to-host copy, which
     synchronises the stream) and a non-zero status raises FrnntStatusError.
     """
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, wgrad_f32=wgrad_f32)
+    if dropout is not None:
+        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd(
+            f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells, blank, out, check,
+            stream, loss, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss, wgrad_f32=wgrad_f32)
     if out is None:
@@ -329,12 +367,16 @@ def fwd_bwd(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=None, mode
 
 def fwd_bwd_noalloc(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=None, mode="tiled", path="auto",
                     chunk_cells=0, blank=0, out: Outputs | None = None, check=True, stream=None,
-                    loss="marginal"):
+                    loss="marginal", dropout: Dropout | None = None):
     """frnnt_fwd_bwd_noalloc: like fwd_bwd, but the library's fixed scratch
     array replaces the workspace (``out.workspace`` is not used).  Raises
     FrnntError(FRNNT_ERR_WORKSPACE) when these dims need more than
     NOALLOC_MAX_BYTES of scratch."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out)
+    if dropout is not None:
+        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_noalloc(
+            f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells, blank, out, check,
+            stream, loss))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss)
     if out is None:
@@ -389,11 +431,15 @@ def set_joint_variant(variant: int) -> int:
 
 def fwd_bwd_pruned(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S: int, grad_loss=None, mode="tiled",
                    path="auto", chunk_cells=0, blank=0, out: Outputs | None = None, check=True, stream=None,
-                   loss="marginal", wgrad_f32=False):
+                   loss="marginal", wgrad_f32=False, dropout: Dropout | None = None):
     """frnnt_fwd_bwd_pruned: the loss and gradients on the pruned lattice that
     keeps, for frame t of utterance b, the S label positions
     bounds[b,t] <= u < bounds[b,t] + S (bounds: int32 [B, T] on the device)."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, bounds=bounds, wgrad_f32=wgrad_f32)
+    if dropout is not None:
+        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_pruned(
+            f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S, grad_loss, mode, path, chunk_cells, blank, out,
+            check, stream, loss, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss, S, wgrad_f32=wgrad_f32)
     if out is None:
@@ -416,7 +462,7 @@ def fwd_bwd_pruned(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S: in
 
 def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durations, grad_loss=None,
                 mode="tiled", chunk_cells=0, blank=0, out: Outputs | None = None, check=True, stream=None,
-                wgrad_f32=False):
+                wgrad_f32=False, dropout: Dropout | None = None):
     """frnnt_fwd_bwd_tdt: the token-and-duration transducer loss and gradients.
 
     W_d [n_dur, H] and b_d [n_dur] are the duration head (bf16, like the other
@@ -425,6 +471,10 @@ def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durati
     and db_d)."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, W_d=W_d, b_d=b_d,
                 wgrad_f32=wgrad_f32)
+    if dropout is not None:
+        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_tdt(
+            f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durations, grad_loss, mode, chunk_cells, blank,
+            out, check, stream, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, "auto", chunk_cells, blank, "marginal", 0, tuple(durations),
                    wgrad_f32=wgrad_f32)

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from oracle import ops_oracle as O
-from rnn_joint_network_02_b200 import frnnt
+from rnn_joint_network_02_b200 import frnnt, synth
+from tests.helpers import compare, run_oracle, to_device
 from tests.test_logprob_gpu import TYPES, close, host
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,71 @@ def test_offsets_past_32_bits(cuda_ok):
     tail = torch.ones(4096, dtype=torch.bfloat16, device="cuda")
     assert torch.equal(x[2 ** 32:], frnnt.dropout(tail, 0.5, 11, 2 ** 29))
     assert not torch.equal(x[2 ** 32:], x[:4096])
+
+
+# ------------------------------------------------------------------ the loss calls' own dropout
+ARGS = ("f", "g", "W_f", "W_g", "W_o", "b_o", "labels", "T_len", "U_len")
+
+
+def _dropped_batch(batch, drop):
+    """The batch with f and g dropped as the call drops them (rounded once to its type), and the factors."""
+    n = batch.f.numel()
+    out, factors = dict(batch.__dict__), []
+    for k, at in (("f", drop.offset), ("g", drop.offset + (n + 7) // 8)):
+        t = getattr(batch, k)
+        keep, scale = O.dropout_mask(t.numel(), drop.p, drop.seed, at)
+        factors.append(torch.from_numpy(keep.reshape(t.shape) * scale))
+        out[k] = (t.double() * factors[-1].float().double()).to(torch.float32).to(t.dtype)
+    return synth.Batch(**out), factors
+
+
+@pytest.mark.parametrize("entry", ["fwd_bwd", "noalloc", "pruned"])
+def test_loss_with_dropout(cuda_ok, entry):
+    """Loss and gradients of the dropped inputs against the oracle; df and dg
+    masked alike (their tolerance is the contract's, on the oracle's masked
+    gradient); the inputs themselves are left alone."""
+    name = "tiny" if entry != "pruned" else "short"
+    batch = synth.workload(name, **({} if name == "tiny" else dict(B=2, T=40, U=8, T_range=(20, 40), U_range=(4, 8))))
+    d, drop = to_device(batch), frnnt.Dropout(0.3, 77, 5)
+    f0 = d["f"].clone()
+    args = [d[k] for k in ARGS]
+    dropped, factors = _dropped_batch(batch, drop)
+    if entry == "pruned":
+        S = 5
+        bounds = synth.diagonal_bounds(batch.T_len, batch.U_len, batch.f.shape[1], S)
+        loss, grads = frnnt.fwd_bwd_pruned(*args, bounds.cuda(), S, dropout=drop)
+        ref = run_oracle(dropped, bounds=bounds.numpy(), S=S)
+    else:
+        loss, grads = (frnnt.fwd_bwd if entry == "fwd_bwd" else frnnt.fwd_bwd_noalloc)(*args, dropout=drop)
+        ref = run_oracle(dropped)
+    ref.df, ref.dg = ref.df * factors[0].numpy(), ref.dg * factors[1].numpy()
+    compare(loss, grads, ref, batch.dtype, extra_note=f"dropout {entry}")
+    assert bool((grads["df"][factors[0].cuda() == 0] == 0).all())
+    assert torch.equal(d["f"], f0)
+
+
+def test_loss_with_dropout_uses_its_outputs_again_and_captures(cuda_ok):
+    """With ``out`` nothing is allocated by the second call, and a captured call
+    draws new numbers as the device state moves on."""
+    batch = synth.workload("short")
+    d = to_device(batch)
+    args = [d[k] for k in ARGS]
+    n = frnnt.Dropout.counters(d["f"], d["g"])
+    want = [frnnt.fwd_bwd(*args, mode="untiled", dropout=frnnt.Dropout(0.2, 9, k * n))[0].clone() for k in range(3)]
+    assert not torch.equal(want[0], want[1])
+    rng = torch.tensor([9, 0], dtype=torch.int64, device="cuda")
+    dims = frnnt.dims_of(d["f"], d["g"], d["W_o"], "bf16", "untiled", "auto", 0, batch.blank)
+    out = frnnt.Outputs(*(d[k] for k in ARGS[:6]), dims)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        loss, _ = frnnt.fwd_bwd(*args, mode="untiled", out=out, stream=stream, dropout=frnnt.Dropout(0.2, rng))
+        stream.synchronize()
+        assert torch.allclose(loss, want[0], rtol=1e-5)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            frnnt.fwd_bwd(*args, mode="untiled", out=out, stream=stream, check=False, dropout=frnnt.Dropout(0.2, rng))
+            rng[1] += n
+        for k in range(3):
+            g.replay()
+            stream.synchronize()
+            assert torch.allclose(out.loss, want[k], rtol=1e-5)
