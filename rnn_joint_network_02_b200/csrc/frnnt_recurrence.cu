@@ -180,10 +180,10 @@ __device__ __forceinline__ Map map_one() { return Map{f2_of(1.f, 1.f), f2_of(0.f
 __device__ __forceinline__ Map then(Map f, Map g) { return Map{f2_mul(g.A, f.A), f2_fma(g.A, f.R, g.R)}; }
 __device__ __forceinline__ uint64_t apply(Map f, uint64_t v) { return f2_fma(f.A, v, f.R); }
 
-// The blocks of a cluster tell each other the map of their chunk: every block
-// sends it to every block's shared memory, where an mbarrier counts the bytes of
-// all CL maps.  Two buffers: a block that sends round r + 2 has received
-// round r + 1 from all, and each sent that after all its threads had read round r.
+// The blocks of a cluster tell each other the map of their chunk: the first warp
+// of every block sends it to every block's shared memory, where an mbarrier
+// counts the bytes of all CL maps.  Two buffers: a warp that sends round r + 2
+// has received round r + 1 from all, and each sent that after it had read round r.
 template <int CL>
 struct Exchange {
   ulonglong2 maps[2][CL][32];
@@ -196,12 +196,13 @@ struct Exchange {
       sm100::fence_barrier_init();
     }
   }
-  __device__ __forceinline__ void send(int r, int rank, int lane, int w, Map m) {
-    if (threadIdx.x == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * 32 * sizeof(ulonglong2));
-    if (w < CL)
+  __device__ __forceinline__ void send(int r, int rank, int lane, Map m) {
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * 32 * sizeof(ulonglong2));
+#pragma unroll
+    for (int k = 0; k < CL; ++k)
       asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
-                       in_cluster(&maps[r & 1][rank][lane], w)),
-                   "l"(m.A), "l"(m.R), "r"(in_cluster(&full[r & 1], w))
+                       in_cluster(&maps[r & 1][rank][lane], k)),
+                   "l"(m.A), "l"(m.R), "r"(in_cluster(&full[r & 1], k))
                    : "memory");
   }
   // The carry after this round; `in`: what enters block `rank`'s chunk.
@@ -281,25 +282,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     for (int i = 0; i < kSteps; ++i) m = then(m, Map{a[i], v[i]});
     run[w][lane] = make_ulonglong2(m.A, m.R);
     __syncthreads();
-    Map before = map_one();       // the runs before this warp's
-    for (int k = 0; k < w; ++k) {
-      const ulonglong2 o = run[k][lane];
-      before = then(before, Map{o.x, o.y});
+    if (w == 0) {   // what enters each run, in the place of its R
+      uint64_t in = carry;
+      if constexpr (CL > 1) {
+        Map all = map_one();
+        for (int k = 0; k < nw; ++k) all = then(all, Map{run[k][lane].x, run[k][lane].y});
+        ex.send(r, rank, lane, all);
+        carry = ex.receive(r, rank, lane, carry, in, status);
+      }
+      if (t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
+      for (int k = 0; k < nw; ++k) {
+        const ulonglong2 o = run[k][lane];
+        run[k][lane].y = in;
+        in = apply(Map{o.x, o.y}, in);
+      }
+      if constexpr (CL == 1) carry = in;
     }
-    Map all = then(before, m);    // the chunk
-    for (int k = w + 1; k < nw; ++k) {
-      const ulonglong2 o = run[k][lane];
-      all = then(all, Map{o.x, o.y});
-    }
-    uint64_t in = carry;
-    if constexpr (CL > 1) {
-      ex.send(r, rank, lane, w, all);
-      carry = ex.receive(r, rank, lane, carry, in, status);
-    } else {
-      carry = apply(all, carry);
-    }
-    if (w == 0 && t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
-    uint64_t s = apply(before, in);
+    __syncthreads();
+    uint64_t s = run[w][lane].y;
     if (VEC && whole && t0 + kSteps <= len) {
       char* base = reinterpret_cast<char*>(h + b * d.h_sb + c0 + (long long)(r * CL + rank) * kChunk * d.h_st);
       const uint32_t step = (uint32_t)d.h_st * (uint32_t)sizeof(T);
@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (CL > 1) cluster_wait();
   for (int r = 0; r < rounds; ++r) {
     const int t0 = chunk_at(r) + w * kSteps;
-    uint64_t v = load_state(t0 < len ? saved : nullptr, (long long)b * nc + t0 / kChunk, d.D, c, live, two);
+    uint64_t v = f2_of(0.f, 0.f);   // (the first warp's)
+    if (w == 0 && t0 < len) v = load_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two);
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     __syncthreads();              // this round's rows are here; the stage before is free
     fetch(r + STAGES - 1);
@@ -393,25 +394,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     run[w][lane] = make_ulonglong2(m.A, m.R);
     back[w][lane] = q;
     __syncthreads();
-    for (int k = 0; k < w; ++k) {
-      const ulonglong2 o = run[k][lane];
-      v = f2_fma(o.x, v, o.y);
+    if (w == 0) {   // what enters each run, in the place of its R and Q
+      uint64_t in = carry;
+      if constexpr (CL > 1) {
+        Map all = map_one();
+        for (int k = nw - 1; k >= 0; --k) all = then(all, Map{run[k][lane].x, back[k][lane]});
+        ex.send(r, rank, lane, all);
+      }
+      for (int k = 0; k < nw; ++k) {
+        const ulonglong2 o = run[k][lane];
+        run[k][lane].y = v;
+        v = apply(Map{o.x, o.y}, v);
+      }
+      if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, status);
+      for (int k = nw - 1; k >= 0; --k) {
+        const uint64_t o = back[k][lane];
+        back[k][lane] = in;
+        in = apply(Map{run[k][lane].x, o}, in);
+      }
+      if constexpr (CL == 1) carry = in;
     }
-    Map after = map_one();        // the runs after this warp's, from the end
-    for (int k = nw - 1; k > w; --k) after = then(after, Map{run[k][lane].x, back[k][lane]});
-    Map all = then(after, Map{m.A, q});
-    for (int k = w - 1; k >= 0; --k) all = then(all, Map{run[k][lane].x, back[k][lane]});
-    uint64_t in = carry;
-    if constexpr (CL > 1) ex.send(r, rank, lane, w, all);
+    __syncthreads();
+    v = run[w][lane].y;
+    q = back[w][lane];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {   // the states again, while the maps travel
+    for (int i = 0; i < kSteps; ++i) {   // the states again
       const uint64_t xv = xs.read(at[0], w * kSteps, i, lane, xk);
       past[i] = f2_fma(xv, f2_of(-1.f, -1.f), v);
       v = f2_fma(a[i], v, f2_mul(s[i], xv));
     }
-    if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, status);
-    else carry = apply(all, carry);
-    q = apply(after, in);
     if (VEC && whole && t0 + kSteps <= len) {
       const long long first = chunk_at(r);
       char* bx = reinterpret_cast<char*>(dx + b * d.dx_sb + c0 + first * d.dx_st);
