@@ -446,26 +446,26 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   }
 }
 
-// A cluster of CL blocks a row.  One block: it takes rows in turn, with the
+// A cluster of CL blocks of W warps a row.  One block: it takes rows in turn, with the
 // next row's vectors on their way.  The warps' statistics (and the maxima of the
 // lanes, over the warps) meet in shared memory, in every block of a cluster;
 // one warp, another each row, finishes the row.  What meets has two places, so
 // that the next row's can be put down while this one's are read.
-template <int CL>
+template <int SHARE>
 struct Meeting {
-  Stats stats[kWarps * CL];
-  float most[kWarps * CL][32];
+  Stats stats[SHARE];
+  float most[SHARE][32];
   uint64_t buffer[kWaiting];
   int count;
 };
-template <typename T, bool TOP, int CL>
-__global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
-  __shared__ Meeting<CL> meetings[CL > 1 ? 1 : 2];
-  __shared__ uint8_t who[kWarps][32];
-  __shared__ __align__(16) float maxima[kWarps][32];
+template <typename T, bool TOP, int CL, int W>
+__global__ void __launch_bounds__(W * 32, 24 / W) logprob_block_kernel(FwdParams p, const T* __restrict__ logits) {
+  constexpr int kShare = W * CL, kStride = kShare * 32 * kVecs;
+  __shared__ Meeting<kShare> meetings[CL > 1 ? 1 : 2];
+  __shared__ uint8_t who[W][32];
+  __shared__ __align__(16) float maxima[W][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * kWarps + w;
-  constexpr int kShare = kWarps * CL, kStride = kShare * 32 * kVecs;
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, g = rank * W + w;
   if (CL > 1) cluster_arrive();
   const long long step = CL > 1 ? p.N : gridDim.x;   // a cluster takes one row
   long long n = blockIdx.x / CL;
@@ -474,11 +474,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_block_kernel(FwdParams
   if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
   float edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : -INFINITY;
   if (threadIdx.x == 0)
-    for (Meeting<CL>& m : meetings) m.count = 0;
+    for (Meeting<kShare>& m : meetings) m.count = 0;
   __syncthreads();
   for (int i = 0; n < p.N; ++i, n += step) {
-    Meeting<CL>& meet = meetings[CL > 1 ? 0 : i & 1];
-    const int writer = CL > 1 ? 0 : i % kWarps;
+    Meeting<kShare>& meet = meetings[CL > 1 ? 0 : i & 1];
+    const int writer = CL > 1 ? 0 : i % W;
     int token = FRNNT_NO_TOKEN;
     float zt = 0.f;
     if (g == writer) {
@@ -838,12 +838,16 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   } else {
     int cl = 1;
     while (cl < 8 && (long long)p.N * cl < 148 && chunks > (long long)kWarps * cl) cl *= 2;
-    const int grid = cl > 1 ? p.N * cl : (p.N < kBlocks ? p.N : kBlocks);
-    auto go = [&](auto kernel) { launch_k(kernel, dim3(grid), dim3(kWarps * 32), 0, st, cl, p, logits); };
-    if (cl == 1) go(logprob_block_kernel<T, TOP, 1>);
-    else if (cl == 2) go(logprob_block_kernel<T, TOP, 2>);
-    else if (cl == 4) go(logprob_block_kernel<T, TOP, 4>);
-    else go(logprob_block_kernel<T, TOP, 8>);
+    auto go = [&](auto kernel, int grid, int warps) {
+      launch_k(kernel, dim3(grid), dim3(warps * 32), 0, st, cl, p, logits);
+    };
+    // with rows enough for it, two warps a block, so that fewer wait for each other at the end of a row (8190 x 32768
+    // bf16: 100 us with 8 warps, 97 with 4, 91 with 2; 16001 x 4097 fp32: 60, 49, 45); 8 get a single row done sooner
+    if (p.N >= 4 * kBlocks) go(logprob_block_kernel<T, TOP, 1, 2>, 4 * kBlocks, 2);
+    else if (cl == 1) go(logprob_block_kernel<T, TOP, 1, kWarps>, p.N < kBlocks ? p.N : kBlocks, kWarps);
+    else if (cl == 2) go(logprob_block_kernel<T, TOP, 2, kWarps>, p.N * 2, kWarps);
+    else if (cl == 4) go(logprob_block_kernel<T, TOP, 4, kWarps>, p.N * 4, kWarps);
+    else go(logprob_block_kernel<T, TOP, 8, kWarps>, p.N * 8, kWarps);
   }
   note_launch();
 }
