@@ -16,7 +16,8 @@
  *   - no workspace is needed;
  *   - `status` may be NULL.  When given, invalid device-side values OR their FRNNT_STATUS_* bits into it: the
  *     call never clears it, the caller does.  After a bit was set the outputs of the rows concerned are
- *     unspecified; no access out of bounds happens either way.
+ *     unspecified; no access out of bounds happens either way.  FRNNT_STATUS_TIMEOUT: a bounded wait of the
+ *     recurrence's blocks for each other gave up.
  * Outputs must not overlap inputs except where a call says so.
  */
 #ifndef FRNNT_OPS_H
@@ -40,7 +41,7 @@ enum {
 /* ------------------------------------------------------------------ token log-probabilities */
 
 typedef struct {
-  int N, V;            /* rows, vocabulary size (both >= 1)                                    */
+  int N, V;            /* rows (1 .. 2^27), vocabulary size (1 .. 2^30)                        */
   int K;               /* given tokens per row, 0 .. FRNNT_MAX_TOKENS                          */
   int top;             /* best alternatives per row, 0 .. min(V, FRNNT_MAX_TOP)                */
   frnnt_dtype dtype;   /* element type of logits and dlogits                                   */
@@ -81,7 +82,7 @@ FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, const void* 
 /* ------------------------------------------------------------------ gated linear recurrence */
 
 typedef struct {
-  int B, T, D;               /* sequences, steps, channels (all >= 1)                          */
+  int B, T, D;               /* sequences (1 .. 65535), steps, channels (1 .. 2^30)            */
   frnnt_dtype dtype;         /* element type of x, gate, h, dh, dx and dgate                   */
   /* strides in elements from one sequence (_sb) and one step (_st) to the next; channels are contiguous.
    * Inputs: any strides >= 0, a step at most 2^30 elements.  Outputs (h, dx, dgate): no two elements may
@@ -114,7 +115,7 @@ FRNNT_API int frnnt_recurrence_bwd(const frnnt_recurrence_dims* d, const void* x
                                    void* dx, void* dgate, float* dh0, int32_t* status, void* stream);
 
 typedef struct {
-  int N, S, D;               /* rows, rows of state, channels (all >= 1)                       */
+  int N, S, D;               /* rows (1 .. 65535), rows of state, channels (1 .. 2^30)        */
   frnnt_dtype dtype;         /* element type of x, gate and h                                  */
   long long x_sn, gate_sn;   /* elements from one row to the next (inputs: >= 0)               */
 } frnnt_step_dims;
@@ -137,7 +138,7 @@ typedef struct {
   long long R, C;            /* rows, elements per row (both >= 1)                             */
   frnnt_dtype dtype;
   long long x_ld, y_ld;      /* elements from one row to the next, >= C                        */
-  float p;                   /* probability of dropping, 0 .. 1; used in 65536ths, rounded     */
+  double p;                  /* probability of dropping, 0 .. 1; used in 65536ths, rounded     */
   uint64_t seed, offset;     /* key, and first counter                                         */
 } frnnt_dropout_dims;
 

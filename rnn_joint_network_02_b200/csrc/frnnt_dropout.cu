@@ -186,7 +186,7 @@ extern "C" FRNNT_API int frnnt_dropout(const frnnt_dropout_dims* d, const void* 
   if (d->dtype != FRNNT_F32 && d->dtype != FRNNT_BF16) return FRNNT_ERR_UNSUPPORTED;
   // (the comparison's negation also refuses a NaN p)
   if (d->R < 1 || d->C < 1 || d->R > (1LL << 40) / d->C || d->x_ld < d->C || d->y_ld < d->C ||
-      !(d->p >= 0.f && d->p <= 1.f))
+      !(d->p >= 0.0 && d->p <= 1.0))
     return FRNNT_ERR_DIMS;
   const size_t es = d->dtype == FRNNT_BF16 ? 2 : 4;
   if ((uintptr_t)x % es || (uintptr_t)y % es || (uintptr_t)rng % 8) return FRNNT_ERR_ALIGN;
@@ -197,7 +197,7 @@ extern "C" FRNNT_API int frnnt_dropout(const frnnt_dropout_dims* d, const void* 
   p.n = d->R * d->C;
   p.x_ld = d->x_ld;
   p.y_ld = d->y_ld;
-  p.limit = (uint32_t)((double)d->p * 65536.0 + 0.5);
+  p.limit = (uint32_t)(d->p * 65536.0 + 0.5);
   p.scale = p.limit < 65536u ? 65536.f / (float)(65536u - p.limit) : 0.f;
   p.seed = d->seed;
   p.offset = d->offset;

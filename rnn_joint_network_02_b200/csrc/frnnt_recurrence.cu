@@ -125,8 +125,9 @@ struct Rows {
   __device__ __forceinline__ void copy(uint32_t dst, const char* row, int j) const {
     const int skew = VEC ? 0 : (int)((uintptr_t)row & 15);
     const int bytes = max(0, min(16, width + skew - 16 * j));   // 0: zeros, nothing is read
-    const char* src = bytes > 0 ? row - skew + 16 * j : first;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(row - skew + (bytes > 0 ? 16 * j : 0)),
+                 "r"(bytes)
+                 : "memory");
   }
   // Where row t0 + i of the stage starts, for read().
   __device__ __forceinline__ uint32_t skew(int t0) const { return VEC ? 0u : (uint32_t)(uintptr_t)(first + t0 * step); }
@@ -461,25 +462,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (rank == 0 && w == 0) store_state(dh0, b, d.D, c, live, two, carry);
 }
 
-template <typename T>
-__global__ void step_kernel(frnnt_step_dims d, const T* x, const T* gate, const float* state, const int32_t* parent,
-                            const uint8_t* advance, T* h, float* new_state, int32_t* status) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+// One step: a thread takes C neighbouring channels of a row in one access an
+// array (4 where all rows are aligned to that, else 1).  Bound by memory, and
+// for a beam's few rows by the launch.
+template <typename T, int C>
+struct alignas(C * sizeof(T)) Channels {
+  T v[C];
+};
+constexpr int kStepThreads = 128;
+template <typename T, int C>
+__global__ void __launch_bounds__(kStepThreads)
+    step_kernel(frnnt_step_dims d, const T* __restrict__ x, const T* __restrict__ gate, const float* state,
+                const int32_t* __restrict__ parent, const uint8_t* __restrict__ advance, T* __restrict__ h,
+                float* new_state, int32_t* status) {
+  const int c = (blockIdx.x * kStepThreads + threadIdx.x) * C;
   const long long n = blockIdx.y;
   if (c >= d.D) return;
+  const bool go = !advance || advance[n];
+  Channels<T, C> xv, gv, out;
+  if (go) {   // before the parent is known
+    gv = *reinterpret_cast<const Channels<T, C>*>(gate + n * d.gate_sn + c);
+    xv = *reinterpret_cast<const Channels<T, C>*>(x + n * d.x_sn + c);
+  }
   int from = (int)n;
   if (parent) {
     from = parent[n];
-    if ((from < 0 || from >= d.S) && status) atomicOr(status, FRNNT_STATUS_INDEX);
+    if ((from < 0 || from >= d.S) && status && c == 0) atomicOr(status, FRNNT_STATUS_INDEX);
     from = clampi(from, 0, d.S - 1);
   }
-  float v = state[(long long)from * d.D + c];
-  if (!advance || advance[n]) {
-    const Gates g = gates_of(f2_of(to_f32<T>(gate[n * d.gate_sn + c]), 0.f));
-    v = fmaf(f2_open(g.a).x, v, f2_open(g.s).x * to_f32<T>(x[n * d.x_sn + c]));
+  Channels<float, C> v = *reinterpret_cast<const Channels<float, C>*>(state + (long long)from * d.D + c);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (go) {
+      const Gates g = gates_of(f2_of(to_f32<T>(gv.v[i]), 0.f));
+      v.v[i] = fmaf(f2_open(g.a).x, v.v[i], f2_open(g.s).x * to_f32<T>(xv.v[i]));
+    }
+    out.v[i] = from_f32<T>(v.v[i]);
   }
-  new_state[n * d.D + c] = v;
-  h[n * d.D + c] = from_f32<T>(v);
+  *reinterpret_cast<Channels<float, C>*>(new_state + n * d.D + c) = v;
+  *reinterpret_cast<Channels<T, C>*>(h + n * d.D + c) = out;
 }
 
 bool dtype_ok(frnnt_dtype t) { return t == FRNNT_F32 || t == FRNNT_BF16; }
@@ -546,14 +567,14 @@ int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... ar
 
 // Rows of 16-byte vectors throughout, and chunks that 32-bit offsets span.
 bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void*> ptrs,
-                std::initializer_list<long long> strides) {
+                std::initializer_list<long long> seqs, std::initializer_list<long long> steps) {
   if (d.D % 2) return false;
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return false;
-  for (long long v : strides)
-    if (v * size_of(d.dtype) % 16) return false;
-  for (long long st : {d.x_st, d.gate_st, d.h_st, d.dh_st, d.dx_st, d.dgate_st})
-    if (st > (1LL << 31) / kChunk / 4) return false;
+  for (long long v : seqs)
+    if (d.B > 1 && v * size_of(d.dtype) % 16) return false;
+  for (long long v : steps)
+    if (d.T > 1 && (v * size_of(d.dtype) % 16 || v > (1LL << 31) / kChunk / 4)) return false;
   return true;
 }
 
@@ -616,7 +637,7 @@ extern "C" FRNNT_API int frnnt_recurrence_fwd(const frnnt_recurrence_dims* d, co
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("recurrence_fwd", st);
-    const bool vec = vectors_ok(*d, {x, gate, h}, {d->x_sb, d->x_st, d->gate_sb, d->gate_st, d->h_sb, d->h_st});
+    const bool vec = vectors_ok(*d, {x, gate, h}, {d->x_sb, d->gate_sb, d->h_sb}, {d->x_st, d->gate_st, d->h_st});
     const int rc = (d->dtype == FRNNT_BF16 ? fwd_of<__nv_bfloat16> : fwd_of<float>)(
         vec, *d, x, gate, lengths, h0, h, h_last, saved, status, st);
     if (rc) return rc;
@@ -639,9 +660,8 @@ extern "C" FRNNT_API int frnnt_recurrence_bwd(const frnnt_recurrence_dims* d, co
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("recurrence_bwd", st);
-    const bool vec = vectors_ok(*d, {x, gate, dh, dx, dgate},
-                              {d->x_sb, d->x_st, d->gate_sb, d->gate_st, d->dh_sb, d->dh_st, d->dx_sb, d->dx_st,
-                               d->dgate_sb, d->dgate_st});
+    const bool vec = vectors_ok(*d, {x, gate, dh, dx, dgate}, {d->x_sb, d->gate_sb, d->dh_sb, d->dx_sb, d->dgate_sb},
+                                {d->x_st, d->gate_st, d->dh_st, d->dx_st, d->dgate_st});
     const int rc = (d->dtype == FRNNT_BF16 ? bwd_of<__nv_bfloat16> : bwd_of<float>)(
         vec, *d, x, gate, lengths, saved, dh, dh_last, dx, dgate, dh0, status, st);
     if (rc) return rc;
@@ -654,7 +674,7 @@ extern "C" FRNNT_API int frnnt_recurrence_step(const frnnt_step_dims* d, const v
                                                void* h, float* new_state, int32_t* status, void* stream) {
   if (!d) return FRNNT_ERR_NULL;
   if (!dtype_ok(d->dtype)) return FRNNT_ERR_UNSUPPORTED;
-  if (d->N < 1 || d->N > 65535 || d->S < 1 || d->D < 1 || d->x_sn < 0 || d->gate_sn < 0 ||
+  if (d->N < 1 || d->N > 65535 || d->S < 1 || d->D < 1 || d->D > (1 << 30) || d->x_sn < 0 || d->gate_sn < 0 ||
       (!parent && d->N > d->S) || (parent && new_state == state))
     return FRNNT_ERR_DIMS;
   if (!x || !gate || !state || !h || !new_state) return FRNNT_ERR_NULL;
@@ -666,13 +686,18 @@ extern "C" FRNNT_API int frnnt_recurrence_step(const frnnt_step_dims* d, const v
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("recurrence_step", st);
-    const dim3 grid((d->D + 127) / 128, d->N);
+    const bool four = d->D % 4 == 0 && d->x_sn % 4 == 0 && d->gate_sn % 4 == 0 && aligned(x, 4 * es) &&
+                      aligned(gate, 4 * es) && aligned(h, 4 * es) && aligned(state, 16) && aligned(new_state, 16);
+    const int each = kStepThreads * (four ? 4 : 1);
+    auto go = [&](auto kernel, auto type) {
+      using T = decltype(type);
+      launch_k(kernel, dim3((d->D + each - 1) / each, d->N), dim3(kStepThreads), 0, st, 1, *d, (const T*)x,
+               (const T*)gate, state, parent, advance, (T*)h, new_state, status);
+    };
     if (d->dtype == FRNNT_BF16)
-      step_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(*d, (const __nv_bfloat16*)x, (const __nv_bfloat16*)gate, state,
-                                                       parent, advance, (__nv_bfloat16*)h, new_state, status);
+      go(four ? step_kernel<__nv_bfloat16, 4> : step_kernel<__nv_bfloat16, 1>, __nv_bfloat16());
     else
-      step_kernel<float><<<grid, 128, 0, st>>>(*d, (const float*)x, (const float*)gate, state, parent, advance,
-                                               (float*)h, new_state, status);
+      go(four ? step_kernel<float, 4> : step_kernel<float, 1>, float());
     note_launch();
   }
   return cudaGetLastError() == cudaSuccess ? FRNNT_OK : FRNNT_ERR_CUDA;

@@ -59,7 +59,7 @@ class StepDims(ctypes.Structure):
 
 class DropoutDims(ctypes.Structure):
     _fields_ = [("R", ctypes.c_longlong), ("C", ctypes.c_longlong), ("dtype", ctypes.c_int),
-                ("x_ld", ctypes.c_longlong), ("y_ld", ctypes.c_longlong), ("p", ctypes.c_float),
+                ("x_ld", ctypes.c_longlong), ("y_ld", ctypes.c_longlong), ("p", ctypes.c_double),
                 ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
@@ -755,7 +755,7 @@ def recurrence(x, gate, lengths=None, h0=None, save=True, out: Recurrence | None
         strides += (T * D, D)
     else:
         strides += _steps("out.h", out.h)
-    status = _status(check and lengths is not None, dev)
+    status = _status(check, dev)
     rc = lib().frnnt_recurrence_fwd(RecurrenceDims(B, T, D, dt, *strides), x.data_ptr(), gate.data_ptr(),
                                     _at(lengths), _at(h0), out.h.data_ptr(), out.h_last.data_ptr(), _at(out.saved),
                                     _at(status), _queue(dev))
@@ -793,7 +793,7 @@ def recurrence_bwd(x, gate, fwd: Recurrence, dh, lengths=None, dh_last=None, out
         strides += (T * D, D, T * D, D)
     else:
         strides += _steps("out dx", out["dx"]) + _steps("out dgate", out["dgate"])
-    status = _status(check and lengths is not None, dev)
+    status = _status(check, dev)
     rc = lib().frnnt_recurrence_bwd(RecurrenceDims(B, T, D, dt, *strides), x.data_ptr(), gate.data_ptr(),
                                     _at(lengths), fwd.saved.data_ptr(), dh.data_ptr(), _at(dh_last),
                                     out["dx"].data_ptr(), out["dgate"].data_ptr(), out["dh0"].data_ptr(),

@@ -104,6 +104,50 @@ def test_forward_and_backward(cuda_ok, N, V, K, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K,top", [(80, 9001, 2, 8), (40, 17000, 1, 20), (1200, 3001, 2, 8), (1900, 9000, 6, 4),
+                                       (9000, 1000, 3, 2), (40000, 48, 2, 3)])
+def test_many_rows(cuda_ok, N, V, K, top, dtype):
+    """The row counts that choose other ways through the kernels, against the
+    definition in torch's float64 (with the oracle's tolerances)."""
+    z, tokens, d = make(N, V, K, top, dtype, seed=20, special=False)
+    r = frnnt.token_logprobs(z, tokens, top=top)
+    dz = frnnt.token_logprobs_bwd(z, tokens, r, **d)
+    w = z.double()
+    lse = torch.logsumexp(w, 1, keepdim=True)
+    lp, p = w - lse, torch.exp(w - lse)
+    entropy = -torch.where(p > 0, p * lp, 0.0).sum(1)
+    near = 4 * O.UNIT + 2.0 ** -23 * (float(w[w > -float("inf")].abs().max()) + np.log(V) + 1)
+    none = tokens == frnnt.NO_TOKEN
+    at = tokens.clamp(min=0).long()
+
+    def check(got, want, tol, what):
+        want = torch.as_tensor(want, dtype=torch.float64, device="cuda")
+        bad = ~((got.double() == want) | ((got.double() - want).abs() <= tol))
+        assert not bool(bad.any()), f"{what}: {int(bad.sum())} values off"
+
+    check(r.lse, lse[:, 0], near, "lse")
+    check(r.entropy, entropy, near * (np.log(V) + 2), "entropy")
+    check(r.logp, torch.where(none, 0.0, lp.gather(1, at)), near, "logp")
+    values, ids = torch.sort(w, dim=1, descending=True, stable=True)
+    assert torch.equal(r.top_ids.long(), ids[:, :top])
+    check(r.top_logp, values[:, :top] - lse, near, "top_logp")
+    coef = torch.where(none, 0.0, d["dlogp"].double())
+    size = coef.abs().sum(1, keepdim=True) + d["dtop"].double().abs().sum(1, keepdim=True)
+    want = -p * (coef.sum(1, keepdim=True) + d["dtop"].double().sum(1, keepdim=True))
+    want.scatter_add_(1, at, coef)
+    want.scatter_add_(1, ids[:, :top], d["dtop"].double())
+    de = d["dentropy"].double()[:, None]
+    safe = torch.where(p > 0, lp, 0.0)
+    want -= de * p * (safe + entropy[:, None])
+    rel = 2 * near
+    tol = 2 * rel * p * (size + de.abs() * (safe.abs() + entropy[:, None] + 1)) + de.abs() * p * near * (np.log(V) + 2)
+    hit = torch.zeros_like(w).scatter_(1, at, 1.0).scatter_(1, ids[:, :top], 1.0)
+    tol = tol + hit * 2.0 ** -21 * size
+    tol = tol + O.HALF_STEP[dtype] * (want.abs() + tol) + 2.0 ** -126
+    check(dz, want, tol, "dlogits")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,shift,out_pad,out_shift", [(8, 0, 8, 0), (3, 0, 0, 0), (0, 1, 0, 0), (1, 2, 5, 3),
                                                          (24, 5, 24, 5), (0, 0, 1, 0)])
 @pytest.mark.parametrize("V", [9, 1024, 2051])

@@ -2,6 +2,8 @@
 backward and the one-step form, over types, lengths (zero, one, long, ragged),
 odd sizes and strides."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -159,6 +161,40 @@ def test_same_bits_every_time_and_captured(cuda_ok):
             assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_two_threads_two_streams(cuda_ok):
+    """Calls from two host threads at once, each on its own stream, with blocks
+    of several clusters waiting for their neighbours."""
+    cases = [make(2, 1400, 100, "bf16", seed=s) for s in (21, 22)]
+    want = []
+    for x, gate, lengths, h0, dh, dl in cases:
+        r = frnnt.recurrence(x, gate, lengths=lengths, h0=h0)
+        want.append((r.h, frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)))
+    torch.cuda.synchronize()
+    got, errors, start = [None, None], [], threading.Barrier(2)
+
+    def worker(i):
+        try:
+            x, gate, lengths, h0, dh, dl = cases[i]
+            s = torch.cuda.Stream()
+            start.wait()
+            for _ in range(10):
+                r = frnnt.recurrence(x, gate, lengths=lengths, h0=h0, check=False, stream=s)
+                d = frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl, check=False, stream=s)
+            s.synchronize()
+            got[i] = (r.h, d)
+        except Exception as e:   # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not errors and all(g is not None for g in got), errors
+    for (h, d), (wh, wd) in zip(got, want):
+        assert torch.equal(h, wh) and all(torch.equal(d[k], wd[k]) for k in wd)
+
+
 def test_offsets_past_32_bits(cuda_ok):
     B, T, D = 2, 40, 32
     x, gate, _, h0, dh, dl = make(B, T, D, "bf16", ragged=False, seed=8)
@@ -180,11 +216,12 @@ def test_offsets_past_32_bits(cuda_ok):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,S,D", [(1, 1, 1), (1, 3, 640), (5, 2, 33), (64, 64, 640), (300, 300, 72), (33, 40, 1027)])
 @pytest.mark.parametrize("form", ["plain", "beam"])
-def test_step(cuda_ok, N, S, D, dtype, form):
+@pytest.mark.parametrize("gap", [0, 1])
+def test_step(cuda_ok, N, S, D, dtype, form, gap):
     g = torch.Generator().manual_seed(N + D)
     t = TYPES[dtype]
-    wide = (torch.randn(N, 2 * D + 1, generator=g) * 2).to(t).cuda()
-    x, gate = wide[:, :D], wide[:, D + 1:]
+    wide = (torch.randn(N, 2 * D + gap, generator=g) * 2).to(t).cuda()
+    x, gate = wide[:, :D], wide[:, D + gap:]
     S = max(S, N) if form == "plain" else S
     state = torch.randn(S, D, generator=g).cuda()
     parent = advance = None
