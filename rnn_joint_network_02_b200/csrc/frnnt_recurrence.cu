@@ -134,9 +134,9 @@ struct Rows {
   // The lane's two channels of row w0 + i; skew0: skew() of row w0.
   __device__ __forceinline__ uint64_t read(const Stage<T>& from, int w0, int i, int lane, uint32_t skew0) const {
     if (VEC) return Pair<T>::open(reinterpret_cast<const typename Pair<T>::Raw*>(from.v[w0 + i])[lane]);
-    const int off = (int)((skew0 + (uint32_t)i * (uint32_t)step) & 15u) / (int)sizeof(T) + 2 * lane;
-    // (the last lanes' channels are past the tile: any value does)
-    const T* q = from.v[w0 + i] + min(off, kPitch - 2);
+    // (the last lanes' channels are past the tile: whatever lies there does)
+    const uint32_t off = ((skew0 + (uint32_t)i * (uint32_t)step) & 15u) + 2 * (uint32_t)sizeof(T) * lane;
+    const T* q = reinterpret_cast<const T*>(reinterpret_cast<const char*>(from.v[w0 + i]) + off);
     return f2_of(to_f32<T>(q[0]), to_f32<T>(q[1]));
   }
 };
@@ -544,10 +544,12 @@ int cluster_of(const frnnt_recurrence_dims& d, int tile) {
 // Chunks in shared memory at a time: three of two arrays, two of three (96 KB of
 // a 16-bit type: two blocks an SM; a block of a 32-bit type has the SM alone).
 constexpr int stages_of(int arrays) { return arrays == 2 ? 3 : 2; }
+// What the last lanes may read past the last row (see Rows::read).
+constexpr int kSlack = 16;
 
 template <typename T, int TILE, int ARRAYS, auto kernel, typename... A>
 int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
-  constexpr int chunk = (int)sizeof(Stage<T>) * ARRAYS, most = chunk * stages_of(ARRAYS);
+  constexpr int chunk = (int)sizeof(Stage<T>) * ARRAYS, most = chunk * stages_of(ARRAYS) + kSlack;
   static std::atomic<bool> ready[kDeviceSlots];
   std::atomic<bool>& here = ready[current_device()];
   if (!here.load(std::memory_order_acquire)) {
@@ -559,7 +561,7 @@ int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... ar
   const dim3 grid((d.D + TILE - 1) / TILE * cl, d.B);
   // one round needs one chunk's memory, and a short one only its rows
   const int rounds = ((d.T + kChunk - 1) / kChunk + cl - 1) / cl;
-  const int bytes = rounds >= stages_of(ARRAYS) ? most : rounds * chunk;
+  const int bytes = rounds >= stages_of(ARRAYS) ? most : rounds * chunk + kSlack;
   launch_k(kernel, grid, dim3(warps * 32), bytes, st, cl, args...);
   note_launch();
   return FRNNT_OK;
