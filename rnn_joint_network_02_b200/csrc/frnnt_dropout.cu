@@ -77,6 +77,9 @@ __device__ __forceinline__ void store(const Group<float>& g, float* p) {
                : "memory");
 }
 
+// Bound by memory: an element is read and written once, while the generator
+// costs 20 wide products a counter, 2.5 an element.  32000 x 1024 fp32: 40 us
+// (6.5 TB/s, the copy rate); a thread per counter with single elements: 136 us.
 // Rows whose groups of 8 elements are whole and aligned: a thread takes whole
 // counters.  With one row (contiguous memory) the last group may be short; the
 // first thread takes its elements one by one.
