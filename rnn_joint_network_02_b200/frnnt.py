@@ -499,48 +499,39 @@ def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durati
 
 # ------------------------------------------------------------------ operators beside the loss (include/frnnt_ops.h)
 # These calls can be a few microseconds long on the GPU, so the host side is kept short: each tensor is checked once and
-# nothing is built that the call does not need.  Two of PyTorch's own shortcuts are used where this build has them: the
-# current stream's handle without a Stream object (0.1 us instead of 2.3), and the caching allocator without the
-# dispatcher (0.8 us a tensor instead of 1.5 to 2.3).
+# nothing is built that the call does not need.  Three of PyTorch's own shortcuts are used where this build has them: the
+# current stream's handle without a Stream object (0.1 us instead of 2.3), the caching allocator without the dispatcher
+# (0.8 us a tensor instead of 1.5 to 2.3), and the current device without the check that CUDA is up (a CUDA tensor is
+# at hand).
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_I32, _F32T = torch.int32, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
+    from torch._C._dynamo.guards import _empty_strided_cuda as _new   # (shape, strides, dtype), on the current device
 except ImportError:
-    _empty_strided_cuda = None
+    def _new(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
 def _float_type(name, t):
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}") from None
-
-
-def _empty(dev, dtype, *shape):
-    """A new dense tensor on any device."""
-    return torch.empty(*shape, dtype=dtype, device=dev)
-
-
-def _empty_here(dev, dtype, *shape):
-    """The same on ``dev``, which is the current device."""
-    if _empty_strided_cuda is None:
-        return _empty(dev, dtype, *shape)
-    n = len(shape)
-    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
-    return _empty_strided_cuda(shape, strides, dtype)
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return dt
 
 
 def _expect(name, t, shape, dtype, dev, dense=True):
     """Refuses a tensor of another shape, type, device or (``dense``) layout than the call needs."""
+    if t.shape == shape and t.dtype is dtype and t.device == dev and (not dense or t.is_contiguous()):
+        return
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(name, t):
@@ -567,7 +558,7 @@ def _elsewhere(dev, stream):
     if dev.type != "cuda":
         raise ValueError("the library computes on the GPU: pass CUDA tensors")
     if stream is None:
-        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return None if _current_device() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the call's tensors on {dev}")
     return torch.cuda.stream(stream)
@@ -601,13 +592,27 @@ class LogProbs:
     the last two are None with top = 0."""
     __slots__ = ("logp", "entropy", "lse", "top_logp", "top_ids")
 
-    def __init__(self, N, K, top, device, new=_empty):
-        f32 = torch.float32
-        self.logp = new(device, f32, N, K) if K else None
-        self.entropy = new(device, f32, N)
-        self.lse = new(device, f32, N)
-        self.top_logp = new(device, f32, N, top) if top else None
-        self.top_ids = new(device, torch.int32, N, top) if top else None
+    def __init__(self, N, K, top, device):
+        def new(dtype, *shape):
+            return torch.empty(shape, dtype=dtype, device=device)
+        self.logp = new(_F32T, N, K) if K else None
+        self.entropy, self.lse = new(_F32T, N), new(_F32T, N)
+        self.top_logp = new(_F32T, N, top) if top else None
+        self.top_ids = new(_I32, N, top) if top else None
+
+    @classmethod
+    def _here(cls, N, K, top):
+        """The same on the current device."""
+        r = cls.__new__(cls)
+        r.logp = _new((N, K), (K, 1), _F32T) if K else None
+        r.entropy = _new((N,), (1,), _F32T)
+        r.lse = _new((N,), (1,), _F32T)
+        if top:
+            r.top_logp = _new((N, top), (top, 1), _F32T)
+            r.top_ids = _new((N, top), (top, 1), _I32)
+        else:
+            r.top_logp = r.top_ids = None
+        return r
 
 
 def _check_logprobs(logits, tokens, top):
@@ -620,7 +625,7 @@ def _check_logprobs(logits, tokens, top):
         if tokens.dim() != 2:
             raise ValueError("tokens must be [N, K]")
         K = tokens.shape[1]
-        _expect("tokens", tokens, (N, K), torch.int32, logits.device)
+        _expect("tokens", tokens, (N, K), _I32, logits.device)
     if not 0 <= top <= min(V, MAX_TOP) or K > MAX_TOKENS:
         raise ValueError(f"at most {MAX_TOKENS} tokens and min(V, {MAX_TOP}) alternatives per row")
     return dt, N, V, K
@@ -656,7 +661,7 @@ def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, chec
         with there:
             return token_logprobs(logits, tokens, top, out, check)
     if out is None:
-        out = LogProbs(N, K, top, dev, _empty_here)
+        out = LogProbs._here(N, K, top)
     status = _status(check and K > 0, dev)
     rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V), logits.data_ptr(), _at(tokens),
                                     _at(out.logp), out.entropy.data_ptr(), out.lse.data_ptr(), _at(out.top_logp),
@@ -690,7 +695,7 @@ def token_logprobs_bwd(logits, tokens, fwd: LogProbs, dlogp=None, dentropy=None,
         with there:
             return token_logprobs_bwd(logits, tokens, fwd, dlogp, dentropy, dtop, out, check)
     if out is None:
-        out = _empty_here(dev, logits.dtype, N, V)
+        out = _new((N, V), (V, 1), logits.dtype)
         ldd = V
     else:
         ldd = _rows("out", out)
@@ -707,10 +712,20 @@ class Recurrence:
     backward call, the states saved every SCAN_CHUNK steps (fp32)."""
     __slots__ = ("h", "h_last", "saved")
 
-    def __init__(self, B, T, D, dtype, device, save=True, new=_empty):
-        self.h = new(device, dtype, B, T, D)
-        self.h_last = new(device, torch.float32, B, D)
-        self.saved = new(device, torch.float32, B, _marks(T), D) if save else None
+    def __init__(self, B, T, D, dtype, device, save=True):
+        self.h = torch.empty((B, T, D), dtype=dtype, device=device)
+        self.h_last = torch.empty((B, D), dtype=_F32T, device=device)
+        self.saved = torch.empty((B, _marks(T), D), dtype=_F32T, device=device) if save else None
+
+    @classmethod
+    def _here(cls, B, T, D, dtype, save):
+        """The same on the current device."""
+        r = cls.__new__(cls)
+        r.h = _new((B, T, D), (T * D, D, 1), dtype)
+        r.h_last = _new((B, D), (D, 1), _F32T)
+        n = _marks(T)
+        r.saved = _new((B, n, D), (n * D, D, 1), _F32T) if save else None
+        return r
 
 
 def _marks(T):
@@ -751,7 +766,7 @@ def recurrence(x, gate, lengths=None, h0=None, save=True, out: Recurrence | None
         with there:
             return recurrence(x, gate, lengths, h0, save, out, check)
     if out is None:
-        out = Recurrence(B, T, D, x.dtype, dev, save, _empty_here)
+        out = Recurrence._here(B, T, D, x.dtype, save)
         strides += (T * D, D)
     else:
         strides += _steps("out.h", out.h)
@@ -788,8 +803,9 @@ def recurrence_bwd(x, gate, fwd: Recurrence, dh, lengths=None, dh_last=None, out
         with there:
             return recurrence_bwd(x, gate, fwd, dh, lengths, dh_last, out, check)
     if out is None:
-        out = dict(dx=_empty_here(dev, x.dtype, B, T, D), dgate=_empty_here(dev, x.dtype, B, T, D),
-                   dh0=_empty_here(dev, torch.float32, B, D))
+        full = (T * D, D, 1)
+        out = dict(dx=_new((B, T, D), full, x.dtype), dgate=_new((B, T, D), full, x.dtype),
+                   dh0=_new((B, D), (D, 1), _F32T))
         strides += (T * D, D, T * D, D)
     else:
         strides += _steps("out dx", out["dx"]) + _steps("out dgate", out["dgate"])
@@ -835,8 +851,8 @@ def recurrence_step(x, gate, state, parent=None, advance=None, out=None, check=T
         with there:
             return recurrence_step(x, gate, state, parent, advance, out, check)
     if out is None:
-        h = _empty_here(dev, x.dtype, N, D)
-        new = _empty_here(dev, torch.float32, N, D)
+        h = _new((N, D), (D, 1), x.dtype)
+        new = _new((N, D), (D, 1), _F32T)
     status = _status(check and parent is not None, dev)
     rc = lib().frnnt_recurrence_step(StepDims(N, S, D, dt, x_sn, gate_sn), x.data_ptr(), gate.data_ptr(),
                                      state.data_ptr(), _at(parent), _at(advance), h.data_ptr(), new.data_ptr(),
@@ -900,7 +916,7 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
         with there:
             return dropout(x, p, seed, offset, out)
     if out is None:
-        out = _empty_here(dev, x.dtype, *x.shape) if 1 <= x.dim() <= 3 else _empty(dev, x.dtype, x.shape)
+        out = _new(x.shape, x.stride(), x.dtype) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=dev)
     mask = (1 << 64) - 1
     rc = lib().frnnt_dropout(DropoutDims(R, C, dt, x_ld, y_ld, p, key & mask, offset & mask), x.data_ptr(),
                              out.data_ptr(), _at(rng), _queue(dev))
