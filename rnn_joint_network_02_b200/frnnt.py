@@ -916,7 +916,7 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
         with there:
             return dropout(x, p, seed, offset, out)
     if out is None:
-        out = _new(x.shape, x.stride(), x.dtype) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _new(tuple(x.shape), x.stride(), x.dtype) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=dev)
     mask = (1 << 64) - 1
     rc = lib().frnnt_dropout(DropoutDims(R, C, dt, x_ld, y_ld, p, key & mask, offset & mask), x.data_ptr(),
                              out.data_ptr(), _at(rng), _queue(dev))
