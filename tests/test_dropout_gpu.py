@@ -165,3 +165,25 @@ def test_loss_with_dropout_uses_its_outputs_again_and_captures(cuda_ok):
             g.replay()
             stream.synchronize()
             assert torch.allclose(out.loss, want[k], rtol=1e-5)
+
+
+@pytest.mark.parametrize("entry", ["fwd_bwd", "tdt"])
+def test_loss_with_dropout_is_the_calls_one_by_one(cuda_ok, entry):
+    """The argument and the separate calls (dropout of f and g, loss, dropout of
+    df and dg) give the same bits of the loss and the same zeros."""
+    batch = synth.workload("short")
+    d, drop = to_device(batch), frnnt.Dropout(0.15, 2 ** 63 + 11, 2 ** 40)
+    args = [d[k] for k in ARGS]
+    kw = {}
+    if entry == "tdt":
+        W_d, b_d = synth.duration_head(batch, len(synth.TDT_DURATIONS), seed=5)
+        args[6:6] = [W_d.cuda(), b_d.cuda()]
+        kw = dict(durations=synth.TDT_DURATIONS)
+    call = frnnt.fwd_bwd_tdt if entry == "tdt" else frnnt.fwd_bwd
+    loss, grads = call(*args, mode="untiled", dropout=drop, **kw)
+    at = drop.offset + (d["f"].numel() + 7) // 8
+    f, g = frnnt.dropout(d["f"], drop.p, drop.seed, drop.offset), frnnt.dropout(d["g"], drop.p, drop.seed, at)
+    want, one = call(f, g, *args[2:], mode="untiled", **kw)
+    assert torch.equal(loss, want)
+    df = frnnt.dropout(one["df"], drop.p, drop.seed, drop.offset)
+    assert torch.equal(grads["df"] == 0, df == 0) and torch.allclose(grads["df"].float(), df.float(), rtol=0.05, atol=1e-4)
