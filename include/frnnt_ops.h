@@ -97,7 +97,7 @@ typedef struct {
  *   h       [B, T, D]   rows t >= lengths[b] are written as 0; x and gate are not read there
  *   h_last  [B, D] fp32 the state after the sequence's last step (h0 for length 0), unrounded
  *   saved   [B, ceil(T / FRNNT_SCAN_CHUNK), D] fp32 or NULL: the states before steps 0, 128, 256, ... that the
- *           backward call starts from
+ *           backward call starts from (those at or past lengths[b] are not written)
  *   h0      [B, D] fp32 or NULL
  * The state is carried in fp32 and rounded only where it is written to h. */
 FRNNT_API int frnnt_recurrence_fwd(const frnnt_recurrence_dims* d, const void* x, const void* gate,

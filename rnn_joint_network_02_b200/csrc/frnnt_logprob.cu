@@ -113,7 +113,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint64_t candidate(float v, int col) { return ((uint64_t)order_key(v) << 32) | (uint32_t)~col; }
 
 // Descending order across the lanes (bitonic): merges of 2, 4, ... 32 sorted runs.
-__device__ __forceinline__ uint64_t exchange(uint64_t x, int lane, int apart, bool keep_larger) {
+__device__ __forceinline__ uint64_t exchange(uint64_t x, int apart, bool keep_larger) {
   const uint64_t y = __shfl_xor_sync(kAll, x, apart);
   return (x > y) == keep_larger ? x : y;
 }
@@ -122,7 +122,7 @@ __device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
   for (int run = 2; run <= 32; run *= 2)
 #pragma unroll
     for (int apart = run / 2; apart > 0; apart /= 2)
-      x = exchange(x, lane, apart, ((lane & apart) == 0) == ((lane & run) == 0 || run == 32));
+      x = exchange(x, apart, ((lane & apart) == 0) == ((lane & run) == 0 || run == 32));
   return x;
 }
 // The 32 largest of two descending lists, descending.
@@ -130,7 +130,7 @@ __device__ __forceinline__ uint64_t merge_desc(uint64_t x, uint64_t y, int lane)
   const uint64_t r = __shfl_xor_sync(kAll, y, 31);   // reversed: the maxima form a bitonic sequence
   x = x > r ? x : r;
 #pragma unroll
-  for (int apart = 16; apart > 0; apart /= 2) x = exchange(x, lane, apart, (lane & apart) == 0);
+  for (int apart = 16; apart > 0; apart /= 2) x = exchange(x, apart, (lane & apart) == 0);
   return x;
 }
 

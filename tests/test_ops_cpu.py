@@ -310,3 +310,23 @@ X3, X2 = torch.zeros(2, 5, 8), torch.zeros(4, 8)
 def test_binding_refuses(call, msg):
     with pytest.raises(ValueError, match=msg):
         call()
+
+
+def test_calls_go_to_the_tensors_device_and_stream(monkeypatch):
+    """The context that a call is made in: none on the current device's current
+    stream, the tensors' device where that is another one, a given stream where
+    it belongs to that device."""
+    monkeypatch.setattr(frnnt, "_current_device", lambda: 0)
+    first, second = torch.device("cuda", 0), torch.device("cuda", 1)
+    assert frnnt._elsewhere(first, None) is None
+    there = frnnt._elsewhere(second, None)
+    assert isinstance(there, torch.cuda.device) and there.idx == 1
+
+    class Stream:
+        device = first
+
+    assert isinstance(frnnt._elsewhere(first, Stream()), torch.cuda.StreamContext)
+    with pytest.raises(ValueError, match="the stream is on"):
+        frnnt._elsewhere(second, Stream())
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        frnnt._elsewhere(torch.device("cpu"), None)

@@ -99,3 +99,29 @@ def test_decoding_steps_follow_the_sequence(cuda_ok):
     ref = O.recurrence(both[:, :, :D].double().cpu().numpy(), both[:, :, D:].double().cpu().numpy())
     assert np.all(np.abs(state.double().cpu().numpy() - ref["h_last"]) <= ref["h_last_tol"])
     assert np.all(np.abs(seq.h_last.double().cpu().numpy() - ref["h_last"]) <= ref["h_last_tol"])
+
+
+def test_a_chain_on_a_side_stream(cuda_ok):
+    """Every call takes the stream it is given, for its work and its outputs, and
+    the chain's results are those of the current stream."""
+    g = torch.Generator().manual_seed(5)
+    both = torch.randn(4, 300, 96, generator=g).cuda()
+    z = torch.randn(64, 3000, generator=g).cuda()
+    tokens, one = torch.randint(0, 3000, (64, 1), generator=g, dtype=torch.int32).cuda(), torch.ones(64, 1).cuda()
+
+    def chain(stream):
+        x, gate = both[:, :, :48], both[:, :, 48:]
+        r = frnnt.recurrence(x, gate, stream=stream)
+        y = frnnt.dropout(r.h, 0.3, 17, stream=stream)
+        d = frnnt.recurrence_bwd(x, gate, r, y, stream=stream)
+        step, _ = frnnt.recurrence_step(both[:, 0, :48], both[:, 0, 48:], r.h_last, stream=stream)
+        lp = frnnt.token_logprobs(z, tokens, top=4, stream=stream)
+        dz = frnnt.token_logprobs_bwd(z, tokens, lp, dlogp=one, stream=stream)
+        return [r.h, y, d["dx"], d["dgate"], d["dh0"], step, lp.logp, lp.top_ids, dz]
+
+    want = chain(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = chain(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
