@@ -1,5 +1,7 @@
 // Token log-probabilities of rows of logits: log-softmax values of given
 // tokens, entropy, the best alternatives, and the gradient of the logits.
+#include <type_traits>
+
 #include "frnnt_common.cuh"
 #include "frnnt_internal.h"
 #include "frnnt_ops.h"
@@ -99,25 +101,45 @@ __device__ __forceinline__ void join_warp(Stats& a) {
 }
 
 // ------------------------------------------------------------------ best alternatives
-// Candidates are ordered by one 64-bit number: the value's order-preserving
-// image above the inverted column, so that equal values rank by column, the
-// lowest first.  NaN ranks below everything; 0 is no candidate.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0u;
-  const uint32_t b = __float_as_uint(v + 0.f);   // -0 becomes +0: they are equal
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
-__device__ __forceinline__ uint64_t candidate(float v, int col) { return ((uint64_t)order_key(v) << 32) | (uint32_t)~col; }
+// Candidates are ordered by one number: the value's order-preserving image above
+// the inverted column, so that equal values rank by column, the lowest first.
+// 0 is no candidate.  Wide: any value (NaN ranks below everything), any column.
+struct Wide {
+  using Key = uint64_t;
+  static __device__ __forceinline__ uint32_t image(float v) {
+    if (v != v) return 0u;
+    const uint32_t b = __float_as_uint(v + 0.f);   // -0 becomes +0: they are equal
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  }
+  static __device__ __forceinline__ float value_of(uint32_t k) {
+    return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+  }
+  static __device__ __forceinline__ Key key(float v, int col) { return ((Key)image(v) << 32) | (uint32_t)~col; }
+  static __device__ __forceinline__ float value(Key k) { return value_of((uint32_t)(k >> 32)); }
+  static __device__ __forceinline__ int column(Key k) { return (int)~(uint32_t)k; }
+};
+// Narrow: 16-bit values other than NaN, columns below 65535, at half the
+// instructions and shared memory.
+struct Narrow {
+  using Key = uint32_t;
+  static __device__ __forceinline__ Key key(float v, int col) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return (((b & 0x80000000u) ? ~b : (b | 0x80000000u)) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)col);
+  }
+  static __device__ __forceinline__ float value(Key k) {
+    return __uint_as_float(((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k) & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ int column(Key k) { return (int)(0xFFFFu - (k & 0xFFFFu)); }
+};
 
 // Descending order across the lanes (bitonic): merges of 2, 4, ... 32 sorted runs.
-__device__ __forceinline__ uint64_t exchange(uint64_t x, int apart, bool keep_larger) {
-  const uint64_t y = __shfl_xor_sync(kAll, x, apart);
+template <typename Key>
+__device__ __forceinline__ Key exchange(Key x, int apart, bool keep_larger) {
+  const Key y = __shfl_xor_sync(kAll, x, apart);
   return (x > y) == keep_larger ? x : y;
 }
-__device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
+template <typename Key>
+__device__ __forceinline__ Key sort_desc(Key x, int lane) {
 #pragma unroll
   for (int run = 2; run <= 32; run *= 2)
 #pragma unroll
@@ -126,26 +148,19 @@ __device__ __forceinline__ uint64_t sort_desc(uint64_t x, int lane) {
   return x;
 }
 // The 32 largest of two descending lists, descending.
-__device__ __forceinline__ uint64_t merge_desc(uint64_t x, uint64_t y, int lane) {
-  const uint64_t r = __shfl_xor_sync(kAll, y, 31);   // reversed: the maxima form a bitonic sequence
+template <typename Key>
+__device__ __forceinline__ Key merge_desc(Key x, Key y, int lane) {
+  const Key r = __shfl_xor_sync(kAll, y, 31);   // reversed: the maxima form a bitonic sequence
   x = x > r ? x : r;
 #pragma unroll
   for (int apart = 16; apart > 0; apart /= 2) x = exchange(x, apart, (lane & apart) == 0);
   return x;
 }
 
-// Candidates wait in shared memory, in any order, until they are sorted.
-constexpr int kWaiting = 256;
-
-// The 32 largest of n <= kWaiting candidates, descending, one a lane.
-__device__ __forceinline__ uint64_t sort_waiting(const uint64_t* buffer, int n, int lane) {
-  uint64_t best = 0;
-  for (int k = 0; k < n; k += 32) {
-    const uint64_t x = sort_desc(k + lane < n ? buffer[k + lane] : 0, lane);
-    best = k ? merge_desc(best, x, lane) : x;
-  }
-  return best;
-}
+// Candidates wait in shared memory, in any order, until they are placed.
+constexpr int kWaitingBytes = 2048;
+template <typename Order>
+constexpr int kWaiting = kWaitingBytes / (int)sizeof(typename Order::Key);
 
 // A value that at least `top` of the row's elements reach, from 32 lanes' maxima
 // of disjoint parts of it: the top-th largest of them, -inf where fewer are
@@ -160,8 +175,8 @@ __device__ __forceinline__ float bound_of(float m, int lane, int top, float* all
     const float4 o = *reinterpret_cast<const float4*>(all + k);
     larger += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
   }
-  const uint32_t kth = __reduce_min_sync(kAll, larger < top ? order_key(m) : 0xFFFFFFFFu);
-  return key_value(kth);
+  const uint32_t kth = __reduce_min_sync(kAll, larger < top ? Wide::image(m) : 0xFFFFFFFFu);
+  return Wide::value_of(kth);
 }
 
 // ------------------------------------------------------------------ forward
@@ -266,8 +281,8 @@ __device__ __forceinline__ void scan_edge(float z, Stats& st) {
 // on the top-th value costs a few reductions, and only what the lanes hold
 // whose largest reaches it is read again (from cache): 32 vectors at a time,
 // one a lane, whichever lane had them.  With random rows 32 ln(32 / (32 - top))
-// elements reach the bound: 9 for the best 8, 31 for 20.  `put` takes a
-// candidate; `who`: 32 places of the warp's own.
+// elements reach the bound: 9 for the best 8, 31 for 20.  `put` takes a value
+// and its column; `who`: 32 places of the warp's own.
 template <typename T, typename Put>
 __device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lane, float most, float bound, float edge,
                                         uint8_t* who, Put put) {
@@ -296,10 +311,10 @@ __device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lan
       const int word = sizeof(T) == 4 ? i : i >> 1;
       uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
       if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
-      put(candidate(__uint_as_float(y), row.head + v * E + i));
+      put(__uint_as_float(y), row.head + v * E + i);
     }
   }
-  if (g == 0 && edge >= bound && row.edge(lane) >= 0) put(candidate(edge, row.edge(lane)));
+  if (g == 0 && edge >= bound && row.edge(lane) >= 0) put(edge, row.edge(lane));
 }
 
 // Rows that the bound does not thin out (many equal values, or fewer than `top`
@@ -312,7 +327,7 @@ __device__ __noinline__ uint64_t best_in_order(const T* p, int V, int top, uint6
   uint64_t best = 0, last = 0;
   int waiting = 0;
   for (int j = 0; j < V || waiting; j += 32) {
-    const uint64_t x = j + lane < V ? candidate(to_f32<T>(__ldg(p + j + lane)), j + lane) : 0;
+    const uint64_t x = j + lane < V ? Wide::key(to_f32<T>(__ldg(p + j + lane)), j + lane) : 0;
     const unsigned from = __ballot_sync(kAll, x > last);
     if (x > last) buffer[waiting + __popc(from & ((1u << lane) - 1))] = x;
     waiting += __popc(from);
@@ -342,29 +357,46 @@ __device__ __forceinline__ void write_token(const FwdParams& p, long long n, int
   if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
   p.logp[n * p.K + k] = !given ? 0.f : st.s == 0.f ? -INFINITY : (z - st.m) - ls;
 }
+template <typename Order>
 __device__ __forceinline__ void write_top(const FwdParams& p, long long n, int place, const Stats& st, float ls,
-                                          uint64_t x) {
+                                          typename Order::Key x) {
   if (place < p.top) {
-    p.top_ids[n * p.top + place] = (int)~(uint32_t)x;
-    p.top_logp[n * p.top + place] = st.s == 0.f ? -INFINITY : (key_value((uint32_t)(x >> 32)) - st.m) - ls;
+    p.top_ids[n * p.top + place] = Order::column(x);
+    p.top_logp[n * p.top + place] = st.s == 0.f ? -INFINITY : (Order::value(x) - st.m) - ls;
   }
 }
 // The row's alternatives from its candidates.  Few: each finds its place by
-// counting the larger ones; more: sorted; too many, or no bound: the row in order.
-template <typename T>
+// counting the larger ones (no step waits for another); more: sorted; too
+// many, or no bound: the row in order.
+template <typename T, typename Order>
 __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int lane, const Stats& st, float ls,
-                                           const T* row, float bound, int found, uint64_t* buffer) {
+                                           const T* row, float bound, int found, unsigned char* waiting) {
+  using Key = typename Order::Key;
+  constexpr int kAtOnce = 16 / sizeof(Key);
+  Key* buffer = reinterpret_cast<Key*>(waiting);
   if (bound > -INFINITY && found <= 64) {
+    if (lane < kAtOnce - 1) buffer[found + lane] = 0;
+    __syncwarp();
     for (int j = lane; j < found; j += 32) {
-      const uint64_t x = buffer[j];
+      const Key x = buffer[j];
       int place = 0;
-      for (int k = 0; k < found; ++k) place += buffer[k] > x;
-      write_top(p, n, place, st, ls, x);
+      for (int k = 0; k < found; k += kAtOnce) {
+        Key o[kAtOnce];
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(buffer + k);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) place += o[i] > x;
+      }
+      write_top<Order>(p, n, place, st, ls, x);
     }
+  } else if (bound > -INFINITY && found <= kWaiting<Order>) {
+    Key best = 0;
+    for (int k = 0; k < found; k += 32) {
+      const Key x = sort_desc<Key>(k + lane < found ? buffer[k + lane] : 0, lane);
+      best = k ? merge_desc<Key>(best, x, lane) : x;
+    }
+    write_top<Order>(p, n, lane, st, ls, best);
   } else {
-    write_top(p, n, lane, st, ls,
-              bound > -INFINITY && found <= kWaiting ? sort_waiting(buffer, found, lane)
-                                                     : best_in_order(row, p.V, p.top, buffer));
+    write_top<Wide>(p, n, lane, st, ls, best_in_order(row, p.V, p.top, reinterpret_cast<uint64_t*>(waiting)));
   }
 }
 
@@ -380,7 +412,8 @@ __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int 
 constexpr int kEarly = 2;
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
-  __shared__ uint64_t buffers[TOP ? kWarps : 1][kWaiting];
+  using Order = std::conditional_t<sizeof(T) == 2, Narrow, Wide>;   // (its rows are shorter than 65535)
+  __shared__ __align__(16) unsigned char waiting[TOP ? kWarps : 1][kWaitingBytes];
   __shared__ int counts[kWarps];
   __shared__ uint8_t who[kWarps][32];
   __shared__ __align__(16) float maxima[kWarps][32];
@@ -430,12 +463,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
       if (lane == 0) counts[w] = 0;
       __syncwarp();
       if (bound > -INFINITY)
-        collect(here, 0, 1, lane, most, bound, z, who[w], [&](uint64_t x) {
+        collect(here, 0, 1, lane, most, bound, z, who[w], [&](float v, int col) {
           const int at = atomicAdd(&counts[w], 1);
-          if (at < kWaiting) buffers[w][at] = x;
+          if (at < kWaiting<Order>) reinterpret_cast<typename Order::Key*>(waiting[w])[at] = Order::key(v, col);
         });
       __syncwarp();
-      finish_top(p, n0 + i, lane, st, logf(st.s), here.p, bound, counts[w], buffers[w]);
+      finish_top<T, Order>(p, n0 + i, lane, st, logf(st.s), here.p, bound, counts[w], waiting[w]);
       __syncwarp();
     }
   }
@@ -463,7 +496,7 @@ template <int SHARE>
 struct Meeting {
   Stats stats[SHARE];
   float most[SHARE][32];
-  uint64_t buffer[kWaiting];
+  __align__(16) unsigned char waiting[kWaitingBytes];
   int count;
 };
 template <typename T, bool TOP, int CL, int W>
@@ -538,18 +571,20 @@ __global__ void __launch_bounds__(W * 32, 24 / W) logprob_block_kernel(FwdParams
       for (int k = 0; k < kShare; ++k) m = fmaxf(m, meet.most[k][lane]);
       bound = bound_of(m, lane, p.top, maxima[w]);
       if (bound > -INFINITY)
-        collect(here, g, kShare, lane, most, bound, z, who[w], [&](uint64_t x) {
+        collect(here, g, kShare, lane, most, bound, z, who[w], [&](float v, int col) {
+          const uint64_t x = Wide::key(v, col);
           if constexpr (CL > 1) {
             uint32_t at;
             asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
                          : "=r"(at)
                          : "r"(in_cluster(&meet.count, 0))
                          : "memory");
-            if (at < kWaiting)
-              asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(&meet.buffer[at], 0)), "l"(x) : "memory");
+            if (at < kWaiting<Wide>)
+              asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(meet.waiting, 0) + 8 * at), "l"(x)
+                           : "memory");
           } else {
             const int at = atomicAdd(&meet.count, 1);
-            if (at < kWaiting) meet.buffer[at] = x;
+            if (at < kWaiting<Wide>) reinterpret_cast<uint64_t*>(meet.waiting)[at] = x;
           }
         });
       if (CL > 1) {
@@ -569,7 +604,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) logprob_block_kernel(FwdParams
       if (lane == 0) write_stats(p, n, st, ls);
       if (lane < p.K) write_token(p, n, lane, st, ls, token, zt);
       if constexpr (TOP) {
-        finish_top(p, n, lane, st, ls, here.p, bound, meet.count, meet.buffer);
+        finish_top<T, Wide>(p, n, lane, st, ls, here.p, bound, meet.count, meet.waiting);
         __syncwarp();
         if (lane == 0) meet.count = 0;
       }
