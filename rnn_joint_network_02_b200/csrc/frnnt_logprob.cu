@@ -224,12 +224,14 @@ __device__ __forceinline__ float vector_max(uint4 r) {
 // The statistics of the first n of a chunk's vectors.  The maximum is taken on
 // the packed elements, which are unpacked once, vector by vector.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st) {
+__device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st, float (&vmax)[kVecs]) {
   constexpr int E = Row<T>::E;
   float m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u)
-    if (WHOLE || u < n) m = fmaxf(m, vector_max<T>(c.v[u]));
+  for (int u = 0; u < kVecs; ++u) {
+    vmax[u] = WHOLE || u < n ? vector_max<T>(c.v[u]) : -INFINITY;
+    m = fmaxf(m, vmax[u]);
+  }
   const float ref = fmaxf(m, st.m);
   if (ref > st.m) rescale(st, ref);
   // a lane that has seen only -inf (or NaN) sums about 0
@@ -256,10 +258,11 @@ __device__ __forceinline__ void scan_chunk(const Chunk& c, int n, Stats& st) {
 
 }
 
+// (vmax: the vectors' maxima)
 template <typename T>
-__device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, Stats& st) {
-  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, true>(c, kVecs, st);
-  else scan_chunk<T, false>(c, (row.nvec - base + 31) / 32, st);
+__device__ __forceinline__ void scan(const Chunk& c, const Row<T>& row, int base, Stats& st, float (&vmax)[kVecs]) {
+  if (base + 32 * kVecs <= row.nvec) scan_chunk<T, true>(c, kVecs, st, vmax);
+  else scan_chunk<T, false>(c, (row.nvec - base + 31) / 32, st, vmax);
 }
 
 // Head and tail: one element a lane (-inf where there is none).
@@ -284,9 +287,27 @@ __device__ __forceinline__ void scan_edge(float z, Stats& st) {
 // elements reach the bound: 9 for the best 8, 31 for 20.  `put` takes a value
 // and its column; `who`: 32 places of the warp's own.
 template <typename T, typename Put>
+__device__ __forceinline__ void collect_vector(const Row<T>& row, int v, float bound, Put put) {
+  constexpr int E = Row<T>::E;
+  const uint4 r = __ldg(row.vec(v));
+  if (!(vector_max<T>(r) >= bound)) return;
+  float z[E];
+  unpack<T>(r, z);
+  unsigned elems = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) elems |= (unsigned)(z[i] >= bound) << i;
+  while (elems) {
+    const int i = __ffs(elems) - 1;
+    elems &= elems - 1;
+    const int word = sizeof(T) == 4 ? i : i >> 1;
+    uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
+    if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
+    put(__uint_as_float(y), row.head + v * E + i);
+  }
+}
+template <typename T, typename Put>
 __device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lane, float most, float bound, float edge,
                                         uint8_t* who, Put put) {
-  constexpr int E = Row<T>::E;
   const unsigned from = __ballot_sync(kAll, most >= bound);
   if (!from) return;
   if (most >= bound) who[__popc(from & ((1u << lane) - 1))] = (uint8_t)lane;
@@ -297,24 +318,27 @@ __device__ __forceinline__ void collect(const Row<T>& row, int g, int G, int lan
   for (int t = lane; t < items; t += 32) {
     const int q = t / kVecs, owner = chunks == 1 ? q : q / chunks;
     const int v = first + (q - owner * chunks) * (G * span) + (t % kVecs) * 32 + who[owner];
-    if (v >= row.nvec) continue;
-    const uint4 r = __ldg(row.vec(v));
-    if (!(vector_max<T>(r) >= bound)) continue;
-    float z[E];
-    unpack<T>(r, z);
-    unsigned elems = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) elems |= (unsigned)(z[i] >= bound) << i;
-    while (elems) {
-      const int i = __ffs(elems) - 1;
-      elems &= elems - 1;
-      const int word = sizeof(T) == 4 ? i : i >> 1;
-      uint32_t y = word == 0 ? r.x : word == 1 ? r.y : word == 2 ? r.z : r.w;
-      if (sizeof(T) == 2) y = (i & 1) ? y & 0xFFFF0000u : y << 16;
-      put(__uint_as_float(y), row.head + v * E + i);
-    }
+    if (v < row.nvec) collect_vector(row, v, bound, put);
   }
   if (g == 0 && edge >= bound && row.edge(lane) >= 0) put(edge, row.edge(lane));
+}
+// A row of one chunk: its vectors' maxima are still at hand, so only the vectors
+// that reach the bound are read again.  `who`: 128 places.
+template <typename T, typename Put>
+__device__ __forceinline__ void collect_short(const Row<T>& row, int lane, const float (&vmax)[kVecs], float bound,
+                                              float edge, uint8_t* who, Put put) {
+  static_assert(32 * kVecs <= 128, "a place for each vector, numbered in a byte");
+  int items = 0;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const bool may = vmax[u] >= bound;
+    const unsigned from = __ballot_sync(kAll, may);
+    if (may) who[items + __popc(from & ((1u << lane) - 1))] = (uint8_t)(u * 32 + lane);
+    items += __popc(from);
+  }
+  __syncwarp();
+  for (int t = lane; t < items; t += 32) collect_vector(row, who[t], bound, put);
+  if (edge >= bound && row.edge(lane) >= 0) put(edge, row.edge(lane));
 }
 
 // Rows that the bound does not thin out (many equal values, or fewer than `top`
@@ -404,7 +428,7 @@ __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int 
 // fp32; bound by the pass over memory (2 bytes a 16-bit element), in practice
 // by what surrounds one exponential an element: 380 instructions a row of 1024,
 // of which 200 are the elements'.  32400 x 1024 bf16: 20 us (3.3 TB/s; a warp a
-// row without a next one on its way: 31 us), with the best 8: 42 us.
+// row without a next one on its way: 31 us), with the best 8: 39 us, 20: 48 us.
 // A warp takes `rows` rows, one after another, with the next one's vectors on
 // their way.  Lane i keeps row i's joined statistics, so that the logarithms,
 // divisions and stores of up to 32 rows are made at once, a lane a row; the
@@ -415,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   using Order = std::conditional_t<sizeof(T) == 2, Narrow, Wide>;   // (its rows are shorter than 65535)
   __shared__ __align__(16) unsigned char waiting[TOP ? kWarps : 1][kWaitingBytes];
   __shared__ int counts[kWarps];
-  __shared__ uint8_t who[kWarps][32];
+  __shared__ uint8_t who[kWarps][32 * kVecs];
   __shared__ __align__(16) float maxima[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long n0 = ((long long)blockIdx.x * kWarps + w) * rows;
@@ -439,6 +463,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   Stats kept{0.f, 0.f, 0.f};
   for (int i = 0; i < count; ++i) {
     Stats st{-INFINITY, 0.f, 0.f};
+    float vmax[kVecs] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     const Row<T> here = row;
     const float z = edge;
     if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
         load_chunk(next, row, 0, lane);
         edge = row.head + row.tail ? load_edge(row, lane) : -INFINITY;
       }
-      if (here.nvec) scan<T>(c, here, base, st);
+      if (here.nvec) scan<T>(c, here, base, st, vmax);
       if (last) break;
     }
     if (here.head + here.tail) scan_edge(z, st);
@@ -462,11 +487,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
       const float bound = bound_of(most, lane, p.top, maxima[w]);
       if (lane == 0) counts[w] = 0;
       __syncwarp();
-      if (bound > -INFINITY)
-        collect(here, 0, 1, lane, most, bound, z, who[w], [&](float v, int col) {
-          const int at = atomicAdd(&counts[w], 1);
-          if (at < kWaiting<Order>) reinterpret_cast<typename Order::Key*>(waiting[w])[at] = Order::key(v, col);
-        });
+      auto put = [&](float v, int col) {
+        const int at = atomicAdd(&counts[w], 1);
+        if (at < kWaiting<Order>) reinterpret_cast<typename Order::Key*>(waiting[w])[at] = Order::key(v, col);
+      };
+      if (bound > -INFINITY) {
+        if (here.nvec <= 32 * kVecs) collect_short(here, lane, vmax, bound, z, who[w], put);
+        else collect(here, 0, 1, lane, most, bound, z, who[w], put);
+      }
       __syncwarp();
       finish_top<T, Order>(p, n0 + i, lane, st, logf(st.s), here.p, bound, counts[w], waiting[w]);
       __syncwarp();
@@ -539,7 +567,8 @@ __global__ void __launch_bounds__(W * 32, 24 / W) logprob_block_kernel(FwdParams
         if (g * 32 * kVecs < row.nvec) load_chunk(next, row, g * 32 * kVecs, lane);
         edge = g == 0 && row.head + row.tail ? load_edge(row, lane) : -INFINITY;
       }
-      if (base < here.nvec) scan<T>(c, here, base, st);
+      float vmax[kVecs];
+      if (base < here.nvec) scan<T>(c, here, base, st, vmax);
       if (base + kStride >= here.nvec) break;
     }
     if (g == 0 && here.head + here.tail) scan_edge(z, st);
