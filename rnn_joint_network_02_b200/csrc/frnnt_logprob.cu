@@ -118,16 +118,15 @@ struct Wide {
   static __device__ __forceinline__ float value(Key k) { return value_of((uint32_t)(k >> 32)); }
   static __device__ __forceinline__ int column(Key k) { return (int)~(uint32_t)k; }
 };
-// Narrow: 16-bit values other than NaN, columns below 65535, at half the
-// instructions and shared memory.
+// Narrow: 16-bit values, columns below 65535, at half the instructions and
+// shared memory.
 struct Narrow {
   using Key = uint32_t;
   static __device__ __forceinline__ Key key(float v, int col) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    return (((b & 0x80000000u) ? ~b : (b | 0x80000000u)) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)col);
+    return (Wide::image(v) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)col);
   }
   static __device__ __forceinline__ float value(Key k) {
-    return __uint_as_float(((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k) & 0xFFFF0000u);
+    return __uint_as_float(((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k) & 0xFFFF0000u);   // (0: a NaN)
   }
   static __device__ __forceinline__ int column(Key k) { return (int)(0xFFFFu - (k & 0xFFFFu)); }
 };
@@ -389,6 +388,20 @@ __device__ __forceinline__ void write_top(const FwdParams& p, long long n, int p
     p.top_logp[n * p.top + place] = st.s == 0.f ? -INFINITY : (Order::value(x) - st.m) - ls;
   }
 }
+// How many of the n candidates (and zeros up to a multiple of 16 bytes) are
+// larger than x.
+template <typename Key>
+__device__ __forceinline__ int larger_than(Key x, const Key* all, int n) {
+  constexpr int kAtOnce = 16 / sizeof(Key);
+  int larger = 0;
+  for (int k = 0; k < n; k += kAtOnce) {
+    Key o[kAtOnce];
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(all + k);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) larger += o[i] > x;
+  }
+  return larger;
+}
 // The row's alternatives from its candidates.  Few: each finds its place by
 // counting the larger ones (no step waits for another); more: sorted; too
 // many, or no bound: the row in order.
@@ -403,14 +416,7 @@ __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int 
     __syncwarp();
     for (int j = lane; j < found; j += 32) {
       const Key x = buffer[j];
-      int place = 0;
-      for (int k = 0; k < found; k += kAtOnce) {
-        Key o[kAtOnce];
-        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(buffer + k);
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) place += o[i] > x;
-      }
-      write_top<Order>(p, n, place, st, ls, x);
+      write_top<Order>(p, n, larger_than(x, buffer, found), st, ls, x);
     }
   } else if (bound > -INFINITY && found <= kWaiting<Order>) {
     Key best = 0;
@@ -509,6 +515,98 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams 
   for (int k = kEarly; k < p.K; ++k) {
     const int t = p.tokens[mine * p.K + k];
     write_token(p, mine, k, kept, ls, t, t >= 0 && t < p.V ? to_f32<T>(__ldg(logits + mine * p.ld + t)) : 0.f);
+  }
+}
+
+// Short rows, where a warp a row would leave most lanes idle: G lanes a row, each
+// with C of its columns, G apart, element by element (any alignment; a warp's
+// rows lie next to each other, so its accesses cover whole sectors all the same).
+// Everything is in registers: bound by the instructions of each element.  60000
+// x 128 bf16: 10.4 us (1.9 TB/s), x 24: 3.3 us.  A candidate for the alternatives
+// finds its place by counting the larger ones: of the whole row, or, with a warp
+// a row, of what reaches the bound.
+template <typename T, int G, int C, bool TOP>
+__global__ void __launch_bounds__(kWarps * 32) logprob_few_kernel(FwdParams p, const T* __restrict__ logits) {
+  using Order = std::conditional_t<sizeof(T) == 2, Narrow, Wide>;
+  using Key = typename Order::Key;
+  constexpr int kRows = 32 / G, kAtOnce = 16 / sizeof(Key);
+  __shared__ __align__(16) Key all[TOP ? kWarps * kRows : 1][G * C + kAtOnce];   // (rows apart in the banks)
+  __shared__ __align__(16) float maxima[TOP && G == 32 ? kWarps : 1][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane % G;
+  const long long first = ((long long)blockIdx.x * kWarps + w) * kRows;
+  if (first >= p.N) return;
+  const bool have = first + lane / G < p.N;
+  const long long n = have ? first + lane / G : p.N - 1;
+  const T* const row = logits + n * p.ld;
+  const int token = g < p.K ? p.tokens[n * p.K + g] : FRNNT_NO_TOKEN;
+  float z[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) z[e] = g + G * e < p.V ? to_f32<T>(__ldg(row + g + G * e)) : -INFINITY;
+  const float zt = token >= 0 && token < p.V ? to_f32<T>(__ldg(row + token)) : 0.f;
+
+  Stats st{-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < C; ++e) st.m = fmaxf(st.m, z[e]);
+  const float most = st.m;   // of this lane's elements
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) st.m = fmaxf(st.m, __shfl_xor_sync(kAll, st.m, o));
+  const float ref = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+  for (int e = 0; e < C; ++e) {
+    const float d = at_least((z[e] - ref) * kLog2e, kFloor), x = exp2_approx(d);
+    st.s += x;
+    st.w = fmaf(x, d, st.w);
+  }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) {
+    st.s += __shfl_xor_sync(kAll, st.s, o);
+    st.w += __shfl_xor_sync(kAll, st.w, o);
+  }
+  const float ls = logf(st.s);
+  if (have) {
+    if (g == 0) write_stats(p, n, st, ls);
+    if (g < p.K) write_token(p, n, g, st, ls, token, zt);
+    for (int k = g + G; k < p.K; k += G) {
+      const int t = p.tokens[n * p.K + k];
+      write_token(p, n, k, st, ls, t, t >= 0 && t < p.V ? to_f32<T>(__ldg(row + t)) : 0.f);
+    }
+  }
+  if constexpr (TOP) {
+    Key* const mine = all[w * kRows + lane / G];
+    const float bound = G == 32 ? bound_of(most, lane, p.top, maxima[w]) : -INFINITY;
+    if (bound > -INFINITY) {
+      int found = 0;
+#pragma unroll
+      for (int e = 0; e < C; ++e) {
+        const bool may = z[e] >= bound;   // (no column behind the last: those are -inf)
+        const unsigned from = __ballot_sync(kAll, may);
+        if (may) mine[found + __popc(from & ((1u << lane) - 1))] = Order::key(z[e], g + G * e);
+        found += __popc(from);
+      }
+      if (lane < kAtOnce - 1) mine[found + lane] = 0;
+      __syncwarp();
+      for (int j = lane; j < found; j += 32) {
+        const Key x = mine[j];
+        write_top<Order>(p, n, larger_than(x, mine, found), st, ls, x);
+      }
+    } else {
+      Key key[C];
+      int place[C] = {};
+#pragma unroll
+      for (int e = 0; e < C; ++e) mine[g + G * e] = key[e] = g + G * e < p.V ? Order::key(z[e], g + G * e) : 0;
+      __syncwarp();
+      for (int k = 0; k < p.V; k += kAtOnce) {
+        Key o[kAtOnce];
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(mine + k);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int e = 0; e < C; ++e) place[e] += o[i] > key[e];
+      }
+#pragma unroll
+      for (int e = 0; e < C; ++e)
+        if (have && g + G * e < p.V) write_top<Order>(p, n, place[e], st, ls, key[e]);
+    }
   }
 }
 
@@ -818,6 +916,43 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdPar
   }
 }
 
+// Short rows: G lanes a row, as in the forward pass.  Every lane goes through the
+// row's coefficients and adds up those of its own columns, so no column is
+// written twice and every element is read and written by one lane (dlogits may be
+// the logits' memory).  60000 x 128 bf16, two tokens and the entropy: 18.4 us, x
+// 24: 4.7 us.
+template <typename T, int G, int C>
+__global__ void __launch_bounds__(kWarps * 32) logprob_bwd_few_kernel(BwdParams p, const T* logits, T* dlogits) {
+  const int lane = threadIdx.x & 31, g = lane % G;
+  const long long n = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / G) + lane / G;
+  if (n >= p.N) return;   // (no lane waits for another)
+  const T* const row = logits + n * p.ld;
+  T* const out = dlogits + n * p.ldd;
+  float z[C], total[C] = {}, sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < C; ++e) z[e] = g + G * e < p.V ? to_f32<T>(row[g + G * e]) : 0.f;
+  const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
+  bool any = p.dentropy != nullptr;
+  const int nk = p.dlogp ? p.K : 0, slots = nk + (p.dtop ? p.top : 0);
+#pragma unroll 2
+  for (int k = 0; k < slots; ++k) {
+    const int t = k < nk ? p.tokens[n * p.K + k] : p.top_ids[n * p.top + k - nk];
+    const float x = k < nk ? p.dlogp[n * p.K + k] : p.dtop[n * p.top + k - nk];
+    if (t >= 0 && t < p.V) {
+      sum += x;
+      any = true;
+#pragma unroll
+      for (int e = 0; e < C; ++e) total[e] += t == g + G * e ? x : 0.f;
+    } else if (g == 0 && !(k < nk && t == FRNNT_NO_TOKEN) && p.status) {
+      atomicOr(p.status, FRNNT_STATUS_LABEL);
+    }
+  }
+  const Slope s{l, -fmaf(de, h, sum), -de * kLn2};
+#pragma unroll
+  for (int e = 0; e < C; ++e)   // a row without any term, or with nothing left by its mask, gets zeros
+    if (g + G * e < p.V) out[g + G * e] = from_f32<T>(!any || l == -INFINITY ? 0.f : s.at(z[e]) + total[e]);
+}
+
 // Any row: `segments` warps share it (no reduction: each needs the row's scalars
 // only).  8190 x 32768 bf16: 170 us (6.3 TB/s, the copy rate).  The columns with coefficients are written
 // again by the warp that wrote them, a lane two slots.
@@ -899,8 +1034,62 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
 // ------------------------------------------------------------------ launches
 constexpr int kBlocks = 148 * 3;   // resident at a time
 
+// Short rows: `go` with the lanes of a row and the columns of a lane.  As many
+// columns as keep the row's reductions few, up to 16; with alternatives a warp a
+// row as soon as counting the whole row costs more than a bound (64 bf16 logits,
+// best 8: 38 us for 60000 rows counted, 28 with a bound).
+using std::integral_constant;
+template <int G, int C, typename Go>
+bool take(Go go) {
+  go(integral_constant<int, G>(), integral_constant<int, C>());
+  note_launch();
+  return true;
+}
+// 60000 rows of 24 / 64 / 128 / 256 / 512 bf16 logits: 3.3 / 5.2 / 10.4 / 15.2 / 25.4 us here, 22 / 23 / 24 / 25 / 28
+// in logprob_warp_kernel (fp32 3.6 / 6.2 / 10.5 / 14.0 / 23.8 and 20 / 21 / 22 / 23 / 24)
+template <typename Go>
+bool with_few_fwd(int V, Go go) {
+  if (V <= 16) return take<2, 8>(go);
+  if (V <= 32) return take<4, 8>(go);
+  if (V <= 64) return take<8, 8>(go);
+  if (V <= 128) return take<16, 8>(go);
+  if (V <= 256) return take<16, 16>(go);
+  return V <= 512 && take<32, 16>(go);
+}
+// with the best 8 alternatives, 24 / 64 / 128 / 256 bf16 logits: 11 / 28 / 32 / 40 us here, 58 / 70 / 60 / 59 there
+template <typename Go>
+bool with_few_top(int V, Go go) {
+  if (V <= 16) return take<4, 4>(go);
+  if (V <= 32) return take<8, 4>(go);
+  if (V <= 64) return take<32, 2>(go);
+  if (V <= 128) return take<32, 4>(go);
+  return V <= 256 && take<32, 8>(go);
+}
+// The gradient, whose every lane goes through all coefficients.  2 of them, 24 / 64 / 128 / 256 logits: 4.7 / 9.5 /
+// 18.4 / 33 us here (256 with 16 columns a lane), 21 / 21 / 23 / 24 in logprob_bwd_rows_kernel; 8 of them, 64 / 128: 15
+// / 27 here, 38 / 41 in logprob_bwd_kernel; 24 of them: 29 / 55 and 48 / 49
+template <typename Go>
+bool with_few_bwd(int V, int slots, Go go) {
+  if (V <= 16) return take<2, 8>(go);
+  if (V <= 32) return take<4, 8>(go);
+  if (V <= 64) return take<8, 8>(go);
+  return V <= 128 && slots <= 16 && take<16, 8>(go);
+}
+inline dim3 few_grid(int N, int G) {
+  const int rows = kWarps * 32 / G;   // of a block
+  return dim3((N + rows - 1) / rows);
+}
+
 template <typename T, bool TOP>
 void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
+  auto few = [&](auto G, auto C) {
+    launch_k(logprob_few_kernel<T, G(), C(), TOP>, few_grid(p.N, G()), dim3(kWarps * 32), 0, st, 1, p, logits);
+  };
+  if constexpr (TOP) {
+    if (with_few_top(p.V, few)) return;
+  } else {
+    if (with_few_fwd(p.V, few)) return;
+  }
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
   if (chunks <= 2 || (chunks < kWarps && p.N >= 148 * kWarps)) {
@@ -931,6 +1120,10 @@ template <typename T>
 void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
   const long long vecs = p.V / (long long)(16 / sizeof(T));
   const int slots = (p.dlogp ? p.K : 0) + (p.dtop ? p.top : 0);
+  auto few = [&](auto G, auto C) {
+    launch_k(logprob_bwd_few_kernel<T, G(), C()>, few_grid(p.N, G()), dim3(kWarps * 32), 0, st, 1, p, logits, dlogits);
+  };
+  if (with_few_bwd(p.V, slots, few)) return;
   if (slots <= kSlots && vecs <= 2 * 32 * kVecs) {
     int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
     if (rows > 32) rows = 32;

@@ -290,3 +290,44 @@ def test_two_threads(cuda_ok):
     assert not errors and all(g is not None for g in got), errors
     for g, w in zip(got, want):
         assert torch.equal(g.logp, w.logp) and torch.equal(g.top_ids, w.top_ids)
+
+
+SHORT = [
+    # N, V, K, top: short rows, one below and one above every change of the lanes a row takes; row counts that end
+    # inside a warp; more tokens than lanes a row; every column an alternative
+    (1, 1, 0, 0), (37, 3, 32, 0), (37, 12, 5, 12), (35, 16, 3, 0), (35, 17, 2, 17), (33, 32, 8, 32), (33, 33, 2, 1),
+    (31, 64, 20, 0), (31, 65, 2, 32), (130, 128, 17, 0), (17, 128, 16, 1), (130, 129, 2, 20), (19, 256, 2, 0),
+    (19, 256, 6, 32), (19, 257, 2, 20), (11, 511, 32, 0), (11, 512, 2, 0), (11, 513, 2, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K,top", SHORT)
+def test_short_rows(cuda_ok, N, V, K, top, dtype):
+    z, tokens, d = make(N, V, K, top, dtype, seed=30, pad=3, shift=1)
+    r = frnnt.token_logprobs(z, tokens, top=top)
+    ref = check_forward(z, tokens, top, r)
+    wide = torch.full((N, V + 5), 5.0, dtype=z.dtype, device="cuda")
+    frnnt.token_logprobs_bwd(z, tokens, r, out=wide[:, 2:2 + V], **d)
+    check_backward(z, tokens, ref, d, wide[:, 2:2 + V], dtype)
+    assert bool((wide[:, :2] == 5).all()) and bool((wide[:, 2 + V:] == 5).all())
+    kept = wide[:, 2:2 + V].clone()
+    frnnt.token_logprobs_bwd(z, tokens, r, out=z, **d)   # in place
+    assert torch.equal(z.isnan(), kept.isnan()) and torch.equal(z.nan_to_num(), kept.nan_to_num())
+
+
+@pytest.mark.parametrize("V", [5, 40, 120])
+def test_short_rows_with_bad_tokens(cuda_ok, V):
+    z, tokens, d = make(6, V, 2, 0, "bf16", special=False)
+    good = frnnt.token_logprobs(z, tokens)
+    wrong = tokens.clone()
+    wrong[4, 1] = V
+    r = frnnt.token_logprobs(z, wrong, check=False)
+    assert r.logp[4, 1] == 0
+    assert torch.equal(r.logp[:4], good.logp[:4]) and torch.equal(r.entropy, good.entropy)
+    with pytest.raises(frnnt.FrnntStatusError) as e:
+        frnnt.token_logprobs(z, wrong)
+    assert e.value.bits == frnnt.STATUS_LABEL
+    with pytest.raises(frnnt.FrnntStatusError) as e:
+        frnnt.token_logprobs_bwd(z, wrong, good, dlogp=d["dlogp"])
+    assert e.value.bits == frnnt.STATUS_LABEL
