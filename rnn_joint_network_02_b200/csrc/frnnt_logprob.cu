@@ -1,5 +1,6 @@
 // Token log-probabilities of rows of logits: log-softmax values of given
 // tokens, entropy, the best alternatives, and the gradient of the logits.
+#include <algorithm>
 #include <type_traits>
 
 #include "frnnt_common.cuh"
@@ -430,27 +431,40 @@ __device__ __forceinline__ void finish_top(const FwdParams& p, long long n, int 
   }
 }
 
+// A warp's share of N rows: warp i of the grid takes rows i N / warps on, so that
+// no two differ by more than one row.  `step`: N / warps in 2^-32, rounded up.
+struct Share {
+  int first, count;
+  __device__ __forceinline__ Share(int N, uint64_t step, int w) {
+    const uint64_t at = (uint64_t)(blockIdx.x * kWarps + w) * step;
+    first = min(N, (int)(at >> 32));
+    count = min(N, (int)((at + step) >> 32)) - first;
+  }
+};
+
 // Rows of a few KB.  One pass over the row with a running maximum and sums in
 // fp32; bound by the pass over memory (2 bytes a 16-bit element), in practice
 // by what surrounds one exponential an element: 380 instructions a row of 1024,
-// of which 200 are the elements'.  32400 x 1024 bf16: 20 us (3.3 TB/s; a warp a
-// row without a next one on its way: 31 us), with the best 8: 39 us, 20: 48 us.
-// A warp takes `rows` rows, one after another, with the next one's vectors on
-// their way.  Lane i keeps row i's joined statistics, so that the logarithms,
+// of which 200 are the elements'.  32400 x 1024 bf16: 18.7 us (3.5 TB/s; with 10
+// rows for most warps instead of 9 or 10 for each: 20.3; a warp a row without a
+// next one on its way: 31), with the best 8: 36 us, 20: 45 us.
+// A warp takes its share of rows, one after another, with the next one's vectors
+// on their way.  Lane i keeps row i's joined statistics, so that the logarithms,
 // divisions and stores of up to 32 rows are made at once, a lane a row; the
 // values of their first tokens are fetched before the rows are scanned.
 constexpr int kEarly = 2;
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, int rows, const T* __restrict__ logits) {
+__global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, uint64_t step, const T* __restrict__ logits) {
   using Order = std::conditional_t<sizeof(T) == 2, Narrow, Wide>;   // (its rows are shorter than 65535)
   __shared__ __align__(16) unsigned char waiting[TOP ? kWarps : 1][kWaitingBytes];
   __shared__ int counts[kWarps];
   __shared__ uint8_t who[kWarps][32 * kVecs];
   __shared__ __align__(16) float maxima[kWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long n0 = ((long long)blockIdx.x * kWarps + w) * rows;
-  if (n0 >= p.N) return;
-  const int count = (int)min((long long)rows, p.N - n0);
+  const Share rows(p.N, step, w);
+  if (!rows.count) return;
+  const long long n0 = rows.first;
+  const int count = rows.count;
   Chunk next;
   Row<T> row(logits + n0 * p.ld, p.V);
   load_chunk(next, row, 0, lane);
@@ -825,20 +839,21 @@ __device__ __forceinline__ void load_vecs(uint4 (&raw)[kVecs], const uint4* src,
 }
 
 // Bound by memory: a row is read and its gradient written.  32400 x 1024 bf16:
-// 24.5 us (5.4 TB/s; a warp a row with its scalars loaded row by row: 34 us).
-// Short rows with few coefficients: a warp takes `rows` rows, one after another,
+// 24.4 us (5.4 TB/s; a warp a row with its scalars loaded row by row: 34 us).
+// Rows of a few KB with few coefficients: a warp takes its share of rows, one after another,
 // with the next one's vectors on their way.  Lane i prepares row i's slope
 // (the loads of up to 32 rows' scalars at once) and, when all rows are
 // written, writes the columns of its tokens again.  Every element is read
 // before it is written, by the same warp, so dlogits may be the logits' memory.
 constexpr int kSlots = 4;
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdParams p, int rows, const T* logits, T* dlogits) {
+__global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdParams p, uint64_t step, const T* logits, T* dlogits) {
   constexpr int E = Row<T>::E;
   const int lane = threadIdx.x & 31;
-  const long long n0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * rows;
-  if (n0 >= p.N) return;
-  const int count = (int)min((long long)rows, p.N - n0);
+  const Share rows(p.N, step, threadIdx.x >> 5);
+  if (!rows.count) return;
+  const long long n0 = rows.first;
+  const int count = rows.count;
   Row<T> row(logits + n0 * p.ld, p.V);
   uint4 next[kVecs];
   load_vecs(next, row.vec(lane), row.nvec - lane);
@@ -1075,6 +1090,17 @@ bool with_few_bwd(int V, int slots, Go go) {
   if (V <= 64) return take<8, 8>(go);
   return V <= 128 && slots <= 16 && take<16, 8>(go);
 }
+// All resident warps, and no more than 32 rows for one.
+struct Rows32 {
+  int blocks;
+  uint64_t step;
+  explicit Rows32(int N) {
+    const int most = (N + kWarps - 1) / kWarps;
+    blocks = most < kBlocks ? most : std::max(kBlocks, (most + 31) / 32);
+    const uint64_t warps = (uint64_t)blocks * kWarps;
+    step = (((uint64_t)N << 32) + warps - 1) / warps;
+  }
+};
 inline dim3 few_grid(int N, int G) {
   const int rows = kWarps * 32 / G;   // of a block
   return dim3((N + rows - 1) / rows);
@@ -1093,12 +1119,8 @@ void launch_fwd(const FwdParams& p, const T* logits, cudaStream_t st) {
   const long long chunk = 32 * kVecs * 16 / sizeof(T);   // a warp's share at a time, in elements
   const long long chunks = (p.V + chunk - 1) / chunk;
   if (chunks <= 2 || (chunks < kWarps && p.N >= 148 * kWarps)) {
-    // as many rows a warp as spread them over the resident warps
-    int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
-    if (rows > 32) rows = 32;
-    const int warps = (p.N + rows - 1) / rows;
-    launch_k(logprob_warp_kernel<T, TOP>, dim3((warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, rows,
-             logits);
+    const Rows32 rows(p.N);
+    launch_k(logprob_warp_kernel<T, TOP>, dim3(rows.blocks), dim3(kWarps * 32), 0, st, 1, p, rows.step, logits);
   } else {
     int cl = 1;
     while (cl < 8 && (long long)p.N * cl < 148 && chunks > (long long)kWarps * cl) cl *= 2;
@@ -1125,11 +1147,8 @@ void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
   };
   if (with_few_bwd(p.V, slots, few)) return;
   if (slots <= kSlots && vecs <= 2 * 32 * kVecs) {
-    int rows = (p.N + kBlocks * kWarps - 1) / (kBlocks * kWarps);
-    if (rows > 32) rows = 32;
-    const int warps = (p.N + rows - 1) / rows;
-    launch_k(logprob_bwd_rows_kernel<T>, dim3((warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, 1, p, rows,
-             logits, dlogits);
+    const Rows32 rows(p.N);
+    launch_k(logprob_bwd_rows_kernel<T>, dim3(rows.blocks), dim3(kWarps * 32), 0, st, 1, p, rows.step, logits, dlogits);
   } else {
     p.segments = vecs <= kSegment ? 1 : (int)((vecs + kSegment - 1) / kSegment);
     const long long warps = (long long)p.N * p.segments;
