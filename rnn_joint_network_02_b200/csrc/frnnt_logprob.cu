@@ -31,19 +31,22 @@ __device__ __forceinline__ float at_least(float x, float lo) {   // a NaN stays
 
 // ------------------------------------------------------------------ rows
 // A row as 16-byte vectors between an unaligned head and a tail, each shorter
-// than a vector.
+// than a vector: those of the row itself, or of the row that it is written to.
 template <typename T>
 struct Row {
   static constexpr int E = 16 / sizeof(T);
   const T* p;
   int head, nvec, tail;
-  __device__ __forceinline__ Row(const T* row, int V) : p(row) {
-    const int off = (int)((uintptr_t)row / sizeof(T) % E);
+  __device__ __forceinline__ Row(const T* row, int V) : Row(row, V, row) {}
+  __device__ __forceinline__ Row(const T* row, int V, const T* to) : p(row) {
+    const int off = (int)((uintptr_t)to / sizeof(T) % E);
     head = min(off ? E - off : 0, V);
     nvec = (V - head) / E;
     tail = V - head - nvec * E;
   }
   __device__ __forceinline__ const uint4* vec(int v) const { return reinterpret_cast<const uint4*>(p + head) + v; }
+  // Bytes from a 16-byte boundary to the first vector.
+  __device__ __forceinline__ int skew() const { return (int)((uintptr_t)(p + head) & 15); }
   // The column of the lane's element of head and tail together, or -1: lanes
   // 0 .. and lanes 8 ..
   __device__ __forceinline__ int edge(int lane) const {
@@ -445,7 +448,7 @@ struct Share {
 // Rows of a few KB.  One pass over the row with a running maximum and sums in
 // fp32; bound by the pass over memory (2 bytes a 16-bit element), in practice
 // by what surrounds one exponential an element: 380 instructions a row of 1024,
-// of which 200 are the elements'.  32400 x 1024 bf16: 18.7 us (3.5 TB/s; with 10
+// of which 200 are the elements'.  32400 x 1024 bf16: 18.3 us (3.6 TB/s; with 10
 // rows for most warps instead of 9 or 10 for each: 20.3; a warp a row without a
 // next one on its way: 31), with the best 8: 36 us, 20: 45 us.
 // A warp takes its share of rows, one after another, with the next one's vectors
@@ -756,36 +759,28 @@ __global__ void __launch_bounds__(W * 32, 24 / W) logprob_block_kernel(FwdParams
 // ------------------------------------------------------------------ backward
 struct BwdParams {
   int N, V, K, top;
-  int segments;            // warps that share a row
+  int segments, share;     // warps that share a row, vectors that one of them takes
   long long ld, ldd;
   const int32_t *tokens, *top_ids;
   const float *lse, *entropy, *dlogp, *dentropy, *dtop;
   int32_t* status;
 };
 
-constexpr int kSegment = 8 * 32 * kVecs;   // vectors of a row that one warp takes: 16 KB
-
 template <typename T>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)], bool whole) {
-  constexpr int E = 16 / sizeof(T);
-  if (whole) {
-    uint4 r;
-    if constexpr (sizeof(T) == 4) {
-      r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    } else {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      r = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    *reinterpret_cast<uint4*>(p) = r;
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)]) {
+  uint4 r;
+  if constexpr (sizeof(T) == 4) {
+    r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   } else {
+    uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    r = make_uint4(u[0], u[1], u[2], u[3]);
   }
+  *reinterpret_cast<uint4*>(p) = r;
 }
 
 // The gradient of a row: dz_j = p_j (A + B log2 p_j) with -A = sum of the
@@ -798,7 +793,7 @@ struct Slope {
     return exp2_approx(d) * fmaf(B, d, A);
   }
   template <typename T>
-  __device__ __forceinline__ void vector(uint4 raw, T* to, bool whole) const {
+  __device__ __forceinline__ void vector(uint4 raw, T* to) const {
     constexpr int E = 16 / sizeof(T);
     const uint64_t l2 = f2_of(-l, -l), l2e = f2_of(kLog2e, kLog2e), A2 = f2_of(A, A), B2 = f2_of(B, B);
     float f[E];
@@ -811,52 +806,105 @@ struct Slope {
       f[i] = g.x;
       f[i + 1] = g.y;
     }
-    store_vec<T>(to, f, whole);
+    store_vec<T>(to, f);
   }
   // kVecs vectors of a lane, 32 apart, those below n
   template <typename T>
-  __device__ __forceinline__ void chunk(const uint4 (&raw)[kVecs], T* to, int n, bool whole) const {
+  __device__ __forceinline__ void chunk(const uint4 (&raw)[kVecs], T* to, int n) const {
     if (n >= 32 * (kVecs - 1) + 1) {
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)), whole);
+      for (int u = 0; u < kVecs; ++u) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)));
     } else {
 #pragma unroll
       for (int u = 0; u < kVecs; ++u)
-        if (32 * u < n) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)), whole);
+        if (32 * u < n) vector<T>(raw[u], to + 32 * u * (16 / (int)sizeof(T)));
     }
   }
 };
+// A lane's vectors, 32 apart, of a warp's share [base, end) of a row.  SKEW: rows
+// may start elsewhere in their 16 bytes than the gradient's.  Then vector v of 16-
+// bit elements lies in two aligned ones, v and v + 1 (both hold some of the row);
+// a lane loads the first of each and shifts it together with the next lane's
+// (8190 x 32768: 202 us; stored element by element instead: 669, aligned: 169).
+// Of 32-bit elements, it loads the four (333 us; shifted: 358, aligned: 326).
 // (plain loads: dlogits may be the logits' memory, and non-coherent ones are for memory that the kernel does not write)
-__device__ __forceinline__ void load_vecs(uint4 (&raw)[kVecs], const uint4* src, int n) {
-  if (n >= 32 * (kVecs - 1) + 1) {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) raw[u] = src[32 * u];
-  } else {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      if (32 * u < n) raw[u] = src[32 * u];
+template <bool SKEW>
+struct Vecs {
+  uint4 raw[kVecs];
+  template <typename T>
+  static __device__ __forceinline__ const uint4* aligned(const Row<T>& row, int skew) {
+    return reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row.p + row.head) - skew);
   }
-}
+  template <typename T>
+  __device__ __forceinline__ void load(const Row<T>& row, int base, int end, int lane) {
+    constexpr bool kShift = SKEW && sizeof(T) == 2;
+    if (base >= end) return;
+    if (SKEW && !kShift && row.skew()) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(row.p + row.head) + 4 * (base + lane);
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u, src += 128)
+        if (32 * u < end - base - lane) raw[u] = make_uint4(src[0], src[1], src[2], src[3]);
+      return;
+    }
+    const int skew = kShift ? row.skew() : 0, n = end - base - lane + (skew != 0);
+    const uint4* src = aligned(row, skew) + base + lane;
+    if (n >= 32 * (kVecs - 1) + 1) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) raw[u] = src[32 * u];
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (32 * u < n) raw[u] = src[32 * u];
+    }
+  }
+  // The vectors from the aligned ones: each with the next lane's, shifted (the
+  // last lane's next one is lane 0's next, or loaded).
+  template <typename T>
+  __device__ __forceinline__ void shift(const Row<T>& row, int base, int end, int lane) {
+    constexpr bool kShift = SKEW && sizeof(T) == 2;
+    const int skew = kShift ? row.skew() : 0;
+    if (skew == 0) return;
+    uint4 behind = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0 && base + 32 * kVecs <= end) behind = aligned(row, skew)[base + 32 * kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const uint4 after = u + 1 < kVecs ? raw[u + 1] : behind;
+      uint32_t w[8] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      w[4] = __shfl_sync(kAll, lane == 0 ? after.x : w[0], (lane + 1) & 31);
+      w[5] = __shfl_sync(kAll, lane == 0 ? after.y : w[1], (lane + 1) & 31);
+      w[6] = __shfl_sync(kAll, lane == 0 ? after.z : w[2], (lane + 1) & 31);
+      w[7] = __shfl_sync(kAll, lane == 0 ? after.w : w[3], (lane + 1) & 31);
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = (skew & 8) ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = (skew & 4) ? w[i + 1] : w[i];
+      const int half = (skew & 2) * 8;
+      raw[u] = make_uint4(__funnelshift_r(w[0], w[1], half), __funnelshift_r(w[1], w[2], half),
+                          __funnelshift_r(w[2], w[3], half), __funnelshift_r(w[3], w[4], half));
+    }
+  }
+};
 
 // Bound by memory: a row is read and its gradient written.  32400 x 1024 bf16:
-// 24.4 us (5.4 TB/s; a warp a row with its scalars loaded row by row: 34 us).
-// Rows of a few KB with few coefficients: a warp takes its share of rows, one after another,
-// with the next one's vectors on their way.  Lane i prepares row i's slope
+// 22.7 us (5.8 TB/s; a warp a row with its scalars loaded row by row: 34 us).
+// Rows of a few KB with few coefficients: a warp takes its share of rows, one
+// after another, with the next one's vectors on their way.  Lane i prepares row i's slope
 // (the loads of up to 32 rows' scalars at once) and, when all rows are
 // written, writes the columns of its tokens again.  Every element is read
 // before it is written, by the same warp, so dlogits may be the logits' memory.
 constexpr int kSlots = 4;
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdParams p, uint64_t step, const T* logits, T* dlogits) {
+template <typename T, bool SKEW>
+__global__ void __launch_bounds__(kWarps * 32, SKEW && sizeof(T) == 2 ? 2 : 3)
+    logprob_bwd_rows_kernel(BwdParams p, uint64_t step, const T* logits, T* dlogits) {
   constexpr int E = Row<T>::E;
   const int lane = threadIdx.x & 31;
   const Share rows(p.N, step, threadIdx.x >> 5);
   if (!rows.count) return;
   const long long n0 = rows.first;
   const int count = rows.count;
-  Row<T> row(logits + n0 * p.ld, p.V);
-  uint4 next[kVecs];
-  load_vecs(next, row.vec(lane), row.nvec - lane);
+  Row<T> row(logits + n0 * p.ld, p.V, dlogits + n0 * p.ldd);
+  Vecs<SKEW> next;
+  next.load(row, 0, row.nvec, lane);
   float edge = row.edge(lane) >= 0 ? to_f32<T>(row.p[row.edge(lane)]) : 0.f;
 
   const long long mine = n0 + lane;
@@ -891,29 +939,27 @@ __global__ void __launch_bounds__(kWarps * 32, 3) logprob_bwd_rows_kernel(BwdPar
     const Row<T> here = row;
     T* const out = dlogits + (n0 + i) * p.ldd;
     T* const body = out + here.head;
-    const bool whole = ((uintptr_t)body & 15u) == 0;
     const float z = edge;
     const int col = here.edge(lane);
-    if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V);
+    if (i + 1 < count) row = Row<T>(logits + (n0 + i + 1) * p.ld, p.V, dlogits + (n0 + i + 1) * p.ldd);
     for (int base = lane;; base += 32 * kVecs) {
-      uint4 raw[kVecs];
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) raw[u] = next[u];
+      Vecs<SKEW> now = next;
       const bool last = base - lane + 32 * kVecs >= here.nvec;
       if (!last) {
-        load_vecs(next, here.vec(base + 32 * kVecs), here.nvec - base - 32 * kVecs);
+        next.load(here, base - lane + 32 * kVecs, here.nvec, lane);
       } else if (i + 1 < count) {
-        load_vecs(next, row.vec(lane), row.nvec - lane);
+        next.load(row, 0, row.nvec, lane);
         if (row.edge(lane) >= 0) edge = to_f32<T>(row.p[row.edge(lane)]);
       }
       T* to = body + (long long)base * E;
       if (g.l != -INFINITY) {
-        g.chunk<T>(raw, to, here.nvec - base, whole);
+        now.shift(here, base - lane, here.nvec, lane);
+        g.chunk<T>(now.raw, to, here.nvec - base);
       } else {   // a row without any term, or with nothing left by its mask, gets zeros
         const float zero[E] = {};
 #pragma unroll
         for (int u = 0; u < kVecs; ++u)
-          if (base + 32 * u < here.nvec) store_vec<T>(to + 32 * u * E, zero, whole);
+          if (base + 32 * u < here.nvec) store_vec<T>(to + 32 * u * E, zero);
       }
       if (last) break;
     }
@@ -969,9 +1015,11 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_few_kernel(BwdParams 
 }
 
 // Any row: `segments` warps share it (no reduction: each needs the row's scalars
-// only).  8190 x 32768 bf16: 170 us (6.3 TB/s, the copy rate).  The columns with coefficients are written
-// again by the warp that wrote them, a lane two slots.
-template <typename T>
+// only), of 16 KB each, or less where there are few (54 x 6769 bf16: 3.3 us; with
+// 16 KB: 7.2).  8190 x 32768 bf16: 169 us (6.4 TB/s, the copy rate).  The columns
+// with coefficients are written again by the warp that wrote them, a lane two
+// slots.
+template <typename T, bool SKEW>
 __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, const T* logits, T* dlogits) {
   constexpr int E = Row<T>::E;
   const int lane = threadIdx.x & 31;
@@ -979,9 +1027,9 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   const long long n = unit / p.segments;
   const int seg = (int)(unit - n * p.segments);
   if (n >= p.N) return;
-  const Row<T> row(logits + n * p.ld, p.V);
   T* out = dlogits + n * p.ldd;
-  const int v0 = seg * kSegment, v1 = min(row.nvec, v0 + kSegment);
+  const Row<T> row(logits + n * p.ld, p.V, out);
+  const int v0 = seg * p.share, v1 = min(row.nvec, v0 + p.share);
 
   // coefficients: slots lane and lane + 32 of the given tokens and the alternatives
   const int nk = p.dlogp ? p.K : 0, count = nk + (p.dtop ? p.top : 0);
@@ -1024,18 +1072,18 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
       if (id[i] >= lo && id[i] < hi) out[id[i]] = from_f32<T>(g.at(zt[i]) + total[i]);
   };
 
-  const bool whole = ((uintptr_t)(out + row.head) & 15u) == 0;
   T* const body = out + row.head;
   if (none) {
     float zero[E] = {};
-    for (int v = v0 + lane; v < v1; v += 32) store_vec<T>(body + (long long)v * E, zero, whole);
+    for (int v = v0 + lane; v < v1; v += 32) store_vec<T>(body + (long long)v * E, zero);
     if (seg == 0 && row.edge(lane) >= 0) out[row.edge(lane)] = from_f32<T>(0.f);
     return;
   }
   for (int base = v0; base < v1; base += 32 * kVecs) {
-    uint4 raw[kVecs];
-    load_vecs(raw, row.vec(base + lane), v1 - base - lane);
-    g.chunk<T>(raw, body + (long long)(base + lane) * E, v1 - base - lane, whole);
+    Vecs<SKEW> now;
+    now.load(row, base, v1, lane);
+    now.shift(row, base, v1, lane);
+    g.chunk<T>(now.raw, body + (long long)(base + lane) * E, v1 - base - lane);
     patch(row.head + base * E, row.head + min(v1, base + 32 * kVecs) * E);
   }
   if (seg == 0 && row.head + row.tail > 0) {
@@ -1146,14 +1194,21 @@ void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
     launch_k(logprob_bwd_few_kernel<T, G(), C()>, few_grid(p.N, G()), dim3(kWarps * 32), 0, st, 1, p, logits, dlogits);
   };
   if (with_few_bwd(p.V, slots, few)) return;
+  // rows of logits and gradient that start at different places of their 16 bytes
+  const bool skewed = (((uintptr_t)logits - (uintptr_t)dlogits) | (uintptr_t)((p.ld - p.ldd) * sizeof(T))) % 16 != 0;
   if (slots <= kSlots && vecs <= 2 * 32 * kVecs) {
     const Rows32 rows(p.N);
-    launch_k(logprob_bwd_rows_kernel<T>, dim3(rows.blocks), dim3(kWarps * 32), 0, st, 1, p, rows.step, logits, dlogits);
+    launch_k(skewed ? logprob_bwd_rows_kernel<T, true> : logprob_bwd_rows_kernel<T, false>, dim3(rows.blocks),
+             dim3(kWarps * 32), 0, st, 1, p, rows.step, logits, dlogits);
   } else {
-    p.segments = vecs <= kSegment ? 1 : (int)((vecs + kSegment - 1) / kSegment);
+    // one to eight chunks a warp, fewer where that gives every SM 16 warps sooner
+    const long long chunks = (vecs + 32 * kVecs - 1) / (32 * kVecs), all = chunks * p.N, enough = all / (148 * 16);
+    const long long most = std::min(8LL, std::max(1LL, enough));
+    p.segments = (int)std::max(1LL, (chunks + most - 1) / most);
+    p.share = 32 * kVecs * (int)((chunks + p.segments - 1) / p.segments);
     const long long warps = (long long)p.N * p.segments;
-    launch_k(logprob_bwd_kernel<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, 1, p,
-             logits, dlogits);
+    launch_k(skewed ? logprob_bwd_kernel<T, true> : logprob_bwd_kernel<T, false>,
+             dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, 1, p, logits, dlogits);
   }
   note_launch();
 }
@@ -1218,7 +1273,7 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs_bwd", st);
-    const BwdParams p{d->N, d->V, d->K, d->top, 1, d->ld, d->ldd, tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,
+    const BwdParams p{d->N, d->V, d->K, d->top, 1, 0, d->ld, d->ldd, tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,
                       status};
     if (d->dtype == FRNNT_BF16) launch_bwd(p, (const __nv_bfloat16*)logits, (__nv_bfloat16*)dlogits, st);
     else launch_bwd(p, (const float*)logits, (float*)dlogits, st);

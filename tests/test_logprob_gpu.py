@@ -331,3 +331,20 @@ def test_short_rows_with_bad_tokens(cuda_ok, V):
     with pytest.raises(frnnt.FrnntStatusError) as e:
         frnnt.token_logprobs_bwd(z, wrong, good, dlogp=d["dlogp"])
     assert e.value.bits == frnnt.STATUS_LABEL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K,top", [(5, 523, 2, 0), (8000, 1027, 2, 0), (7500, 1500, 1, 2), (6, 1030, 5, 3),
+                                       (3, 40001, 2, 0), (4, 1, 1, 1), (4, 7, 2, 0)])
+@pytest.mark.parametrize("pad,shift,out_pad,out_shift", [(3, 0, 0, 0), (0, 0, 3, 1), (1, 2, 5, 3), (4, 4, 0, 0)])
+def test_gradient_elsewhere_in_its_16_bytes(cuda_ok, N, V, K, top, pad, shift, out_pad, out_shift, dtype):
+    """Rows of logits and of the gradient that start at different places of their 16 bytes: the bits are those of
+    dense rows, and nothing around the gradient's rows is written."""
+    z, tokens, d = make(N, V, K, top, dtype, seed=40, pad=pad, shift=shift)
+    r = frnnt.token_logprobs(z, tokens, top=top)
+    want = frnnt.token_logprobs_bwd(z.contiguous(), tokens, r, **d)
+    wide = torch.full((N, out_shift + V + out_pad), 5.0, dtype=z.dtype, device="cuda")
+    got = frnnt.token_logprobs_bwd(z, tokens, r, out=wide[:, out_shift:out_shift + V], **d)
+    raw = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(got.contiguous().view(raw), want.view(raw))
+    assert bool((wide[:, :out_shift] == 5).all()) and bool((wide[:, out_shift + V:] == 5).all())
