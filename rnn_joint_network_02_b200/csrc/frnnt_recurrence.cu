@@ -12,8 +12,9 @@ namespace frnnt {
 namespace {
 
 // A block walks along one sequence, 64 channels wide, kChunk steps at a
-// time.  Lane l of every warp holds channels 2l and 2l + 1; warp w takes the
-// kSteps steps from w * kSteps on.
+// time.  Lane l of every warp holds channels 2l and 2l + 1 (of unaligned rows l
+// and l + half the tile: see kApart); warp w takes the kSteps steps from w *
+// kSteps on.
 constexpr int kChunk = FRNNT_SCAN_CHUNK;
 constexpr int kSteps = 16;
 constexpr int kWarps = kChunk / kSteps;
@@ -77,6 +78,10 @@ struct Pair<__nv_bfloat16> {
 constexpr int kPitch = 64;
 template <typename T, bool VEC>
 constexpr int kTile = VEC ? kPitch : kPitch - 16 / (int)sizeof(T);
+// From a lane's first channel to its second.  Unaligned rows are read and written
+// one element at a time, so those of neighbouring lanes are neighbours.
+template <typename T, bool VEC>
+constexpr int kApart = VEC ? 1 : kTile<T, VEC> / 2;
 
 template <typename T>
 struct Stage {
@@ -135,9 +140,9 @@ struct Rows {
   __device__ __forceinline__ uint64_t read(const Stage<T>& from, int w0, int i, int lane, uint32_t skew0) const {
     if (VEC) return Pair<T>::open(reinterpret_cast<const typename Pair<T>::Raw*>(from.v[w0 + i])[lane]);
     // (the last lanes' channels are past the tile: whatever lies there does)
-    const uint32_t off = ((skew0 + (uint32_t)i * (uint32_t)step) & 15u) + 2 * (uint32_t)sizeof(T) * lane;
+    const uint32_t off = ((skew0 + (uint32_t)i * (uint32_t)step) & 15u) + (uint32_t)sizeof(T) * lane;
     const T* q = reinterpret_cast<const T*>(reinterpret_cast<const char*>(from.v[w0 + i]) + off);
-    return f2_of(to_f32<T>(q[0]), to_f32<T>(q[1]));
+    return f2_of(to_f32<T>(q[0]), to_f32<T>(q[kApart<T, VEC>]));
   }
 };
 // Neutral rows: with gate = +inf, a = 1 and 1 - a = 0, and the state stays as it is.
@@ -156,21 +161,24 @@ __device__ __forceinline__ void store_pair(T* p, float2 v, bool two) {
     *reinterpret_cast<Raw*>(p) = Pair<T>::pack(v);
   } else {
     p[0] = from_f32<T>(v.x);
-    if (two) p[1] = from_f32<T>(v.y);
+    if (two) p[kApart<T, VEC>] = from_f32<T>(v.y);
   }
 }
 
-// Per-sequence channels c and c + 1 of a [rows, D] fp32 array.
+// The lane's channels of a [rows, D] fp32 array.
+template <int APART>
 __device__ __forceinline__ uint64_t load_state(const float* p, long long row, int D, int c, bool live, bool two) {
   if (!p || !live) return f2_of(0.f, 0.f);
   const float* q = p + row * D + c;
-  return f2_of(q[0], two ? q[1] : 0.f);
+  return f2_of(q[0], two ? q[APART] : 0.f);
 }
+template <int APART>
 __device__ __forceinline__ void store_state(float* p, long long row, int D, int c, bool live, bool two, uint64_t v) {
   if (!p || !live) return;
   const float2 f = f2_open(v);
-  p[row * D + c] = f.x;
-  if (two) p[row * D + c + 1] = f.y;
+  float* q = p + row * D + c;
+  q[0] = f.x;
+  if (two) q[APART] = f.y;
 }
 
 // A run of steps as a map of its entering value: out = A in + R.
@@ -250,8 +258,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
-  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D, whole = c0 + kPitch <= d.D;
+  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + (VEC ? 2 : 1) * lane;
+  const bool live = lane < kTile<T, VEC> / 2 && c < d.D, two = c + kApart<T, VEC> < d.D, whole = c0 + kPitch <= d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
   const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D);
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   };
 #pragma unroll
   for (int r = 0; r < STAGES - 1; ++r) fetch(r);
-  uint64_t carry = load_state(h0, b, d.D, c, live, two);
+  uint64_t carry = load_state<kApart<T, VEC>>(h0, b, d.D, c, live, two);
   if (CL > 1) cluster_wait();     // the other blocks run, their mbarriers are ready
   for (int r = 0; r < rounds; ++r) {
     const int t0 = (r * CL + rank) * kChunk + w * kSteps;
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         ex.send(r, rank, lane, all);
         carry = ex.receive(r, rank, lane, carry, in, status);
       }
-      if (t0 < len) store_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
+      if (t0 < len) store_state<kApart<T, VEC>>(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
       for (int k = 0; k < nw; ++k) {
         const ulonglong2 o = run[k][lane];
         run[k][lane].y = in;
@@ -316,6 +324,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         s = f2_fma(a[i], s, v[i]);
         store_at<T>(base, off, s);
       }
+    } else if (!VEC && t0 + kSteps <= len) {
+      T* out = hp + (long long)t0 * d.h_st;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i, out += d.h_st) {
+        s = f2_fma(a[i], s, v[i]);
+        if (live) store_pair<T, VEC>(out, f2_open(s), two);
+      }
     } else {
       T* out = hp + (long long)t0 * d.h_st;
 #pragma unroll
@@ -329,7 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // rows of whole rounds past the sequence
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
     if (live) store_pair<T, VEC>(hp + t * d.h_st, make_float2(0.f, 0.f), two);
-  if (rank == 0 && w == 0) store_state(h_last, b, d.D, c, live, two, carry);
+  if (rank == 0 && w == 0) store_state<kApart<T, VEC>>(h_last, b, d.D, c, live, two, carry);
 }
 
 // Backward.  With q_t = a_t g_t, what step t hands to step t - 1, q_t = a_t
@@ -352,8 +367,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ Exchange<CL> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, rank = CL > 1 ? blockIdx.x % CL : 0;
-  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + 2 * lane;
-  const bool live = 2 * lane < kTile<T, VEC> && c < d.D, two = c + 1 < d.D, whole = c0 + kPitch <= d.D;
+  const int c0 = (blockIdx.x / CL) * kTile<T, VEC>, c = c0 + (VEC ? 2 : 1) * lane;
+  const bool live = lane < kTile<T, VEC> / 2 && c < d.D, two = c + kApart<T, VEC> < d.D, whole = c0 + kPitch <= d.D;
   const int len = length_of(lengths, b, d.T, status), nc = (d.T + kChunk - 1) / kChunk;
   const int rounds = ((len + kChunk - 1) / kChunk + CL - 1) / CL;
   const Rows<T, VEC> xs(x + b * d.x_sb, d.x_st, c0, d.D), gs(gate + b * d.gate_sb, d.gate_st, c0, d.D),
@@ -376,12 +391,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   };
 #pragma unroll
   for (int r = 0; r < STAGES - 1; ++r) fetch(r);
-  uint64_t carry = load_state(dh_last, b, d.D, c, live, two);
+  uint64_t carry = load_state<kApart<T, VEC>>(dh_last, b, d.D, c, live, two);
   if (CL > 1) cluster_wait();
   for (int r = 0; r < rounds; ++r) {
     const int t0 = chunk_at(r) + w * kSteps;
     uint64_t v = f2_of(0.f, 0.f);   // (the first warp's)
-    if (w == 0 && t0 < len) v = load_state(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two);
+    if (w == 0 && t0 < len) v = load_state<kApart<T, VEC>>(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two);
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     __syncthreads();              // this round's rows are here; the stage before is free
     fetch(r + STAGES - 1);
@@ -446,6 +461,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         store_at<T>(bx, ox, f2_mul(s[i], g));
         store_at<T>(bg, og, f2_mul(f2_mul(q, s[i]), past[i]));
       }
+    } else if (!VEC && t0 + kSteps <= len) {
+      T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
+      T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
+#pragma unroll
+      for (int i = kSteps - 1; i >= 0; --i, px -= d.dx_st, pg -= d.dgate_st) {
+        const uint64_t g = f2_add(q, hs.read(at[2], w * kSteps, i, lane, hk));
+        q = f2_mul(a[i], g);
+        if (live) {
+          store_pair<T, VEC>(px, f2_open(f2_mul(s[i], g)), two);
+          store_pair<T, VEC>(pg, f2_open(f2_mul(f2_mul(q, s[i]), past[i])), two);
+        }
+      }
     } else {
       T* px = dxp + (t0 + kSteps - 1) * d.dx_st;
       T* pg = dgp + (t0 + kSteps - 1) * d.dgate_st;
@@ -467,7 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       store_pair<T, VEC>(dxp + t * d.dx_st, make_float2(0.f, 0.f), two);
       store_pair<T, VEC>(dgp + t * d.dgate_st, make_float2(0.f, 0.f), two);
     }
-  if (rank == 0 && w == 0) store_state(dh0, b, d.D, c, live, two, carry);
+  if (rank == 0 && w == 0) store_state<kApart<T, VEC>>(dh0, b, d.D, c, live, two, carry);
 }
 
 // One step: a thread takes C neighbouring channels of a row in one access an
