@@ -1,7 +1,9 @@
 // Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t, a = sigmoid(gate):
 // forward over padded sequences, backward, and one step of many hypotheses.
 #include <atomic>
+#include <climits>
 #include <initializer_list>
+#include <type_traits>
 
 #include "frnnt_common.cuh"
 #include "frnnt_internal.h"
@@ -567,40 +569,82 @@ int check(const frnnt_recurrence_dims* d, bool bwd) {
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 size_t size_of(frnnt_dtype t) { return t == FRNNT_BF16 ? 2 : 4; }
 
-// Blocks that share a sequence's chunks: as many as bring the grid up to the
-// SMs (16-bit: two blocks an SM; 32-bit: one, so half as many, or the blocks
-// would run in two waves: 2 x 16384 x 1024 fp32 77 us with 4, 119 us with 8).
-int cluster_of(const frnnt_recurrence_dims& d, int tile) {
-  const long long tiles = (long long)((d.D + tile - 1) / tile) * d.B;
-  const int nc = (d.T + kChunk - 1) / kChunk;
-  const int fill = d.dtype == FRNNT_BF16 ? 148 : 74;
-  int cl = 1;
-  while (cl < 8 && cl < nc && tiles * cl < fill) cl *= 2;
-  return cl;
-}
-
 // Chunks in shared memory at a time: three of two arrays, two of three (96 KB of
 // a 16-bit type: two blocks an SM; a block of a 32-bit type has the SM alone).
 constexpr int stages_of(int arrays) { return arrays == 2 ? 3 : 2; }
 // What the last lanes may read past the last row (see Rows::read).
 constexpr int kSlack = 16;
 
-template <typename T, int TILE, int ARRAYS, auto kernel, typename... A>
-int launch_scan(const frnnt_recurrence_dims& d, int cl, cudaStream_t st, A... args) {
-  constexpr int chunk = (int)sizeof(Stage<T>) * ARRAYS, most = chunk * stages_of(ARRAYS) + kSlack;
-  static std::atomic<bool> ready[kDeviceSlots];
-  std::atomic<bool>& here = ready[current_device()];
-  if (!here.load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-      return FRNNT_ERR_CUDA;
-    here.store(true, std::memory_order_release);
+template <typename T, int ARRAYS>
+constexpr int kMostBytes = (int)sizeof(Stage<T>) * ARRAYS * stages_of(ARRAYS) + kSlack;
+
+// How many clusters of CL blocks run at a time on the current device (any number
+// with CL = 1), and the kernel made ready for that much shared memory; -1: failed.
+template <typename T, int ARRAYS, int CL, auto kernel>
+int resident() {
+  static std::atomic<int> known[kDeviceSlots];   // (+ 1)
+  std::atomic<int>& here = known[current_device()];
+  if (const int n = here.load(std::memory_order_acquire)) return n - 1;
+  constexpr int bytes = kMostBytes<T, ARRAYS>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -1;
+  int n = INT_MAX - 1;
+  if (CL > 1) {
+    cudaLaunchAttribute size;
+    size.id = cudaLaunchAttributeClusterDimension;
+    size.val.clusterDim.x = CL;
+    size.val.clusterDim.y = size.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(CL);
+    config.blockDim = dim3(kWarps * 32);
+    config.dynamicSmemBytes = bytes;
+    config.attrs = &size;
+    config.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &config) != cudaSuccess || n < 0) return -1;
   }
+  here.store(n + 1, std::memory_order_release);
+  return n;
+}
+
+// Blocks that share a sequence's chunks: as few as give the fewest rounds, of
+// those whose clusters run all at once.  (Clusters of 6 are why 8 x 1500 x 513
+// bf16 takes 17 us and 27 us backward: 23 and 38 with 4; but 3 x 10000 x 1024,
+// whose 48 do not all fit, 61 us and 94 with 6, 55 and 85 with 4.)
+template <typename Fit, typename Launch>
+int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launch) {
+  const long long tiles = (long long)((d.D + tile - 1) / tile) * d.B;
+  const int nc = (d.T + kChunk - 1) / kChunk;
+  auto rounds = [&](int cl) { return (nc + cl - 1) / cl; };
+  int best = 1;
+  auto may = [&](auto CL) {
+    if (tiles * CL() <= 2 * 148 && rounds(CL()) < rounds(best) && tiles <= fit(CL)) best = CL();
+  };
+  using std::integral_constant;
+  may(integral_constant<int, 2>());
+  may(integral_constant<int, 3>());
+  may(integral_constant<int, 4>());
+  may(integral_constant<int, 5>());
+  may(integral_constant<int, 6>());
+  may(integral_constant<int, 8>());
+  switch (best) {
+    case 1: return launch(integral_constant<int, 1>());
+    case 2: return launch(integral_constant<int, 2>());
+    case 3: return launch(integral_constant<int, 3>());
+    case 4: return launch(integral_constant<int, 4>());
+    case 5: return launch(integral_constant<int, 5>());
+    case 6: return launch(integral_constant<int, 6>());
+    default: return launch(integral_constant<int, 8>());
+  }
+}
+
+template <typename T, int TILE, int ARRAYS, int CL, auto kernel, typename... A>
+int launch_scan(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
+  if (resident<T, ARRAYS, CL, kernel>() < 0) return FRNNT_ERR_CUDA;
   const int warps = d.T < kChunk ? (d.T + kSteps - 1) / kSteps : kWarps;
-  const dim3 grid((d.D + TILE - 1) / TILE * cl, d.B);
+  const dim3 grid((d.D + TILE - 1) / TILE * CL, d.B);
   // one round needs one chunk's memory, and a short one only its rows
-  const int rounds = ((d.T + kChunk - 1) / kChunk + cl - 1) / cl;
-  const int bytes = rounds >= stages_of(ARRAYS) ? most : rounds * chunk + kSlack;
-  launch_k(kernel, grid, dim3(warps * 32), bytes, st, cl, args...);
+  const int rounds = ((d.T + kChunk - 1) / kChunk + CL - 1) / CL;
+  const int bytes = rounds >= stages_of(ARRAYS) ? kMostBytes<T, ARRAYS> : rounds * (int)sizeof(Stage<T>) * ARRAYS + kSlack;
+  launch_k(kernel, grid, dim3(warps * 32), bytes, st, CL, args...);
   note_launch();
   return FRNNT_OK;
 }
@@ -620,24 +664,22 @@ bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void
 
 template <typename T, bool VEC, typename... A>
 int scan_fwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
-  constexpr int S = stages_of(2);
-  switch (cluster_of(d, kTile<T, VEC>)) {
-    case 1: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
-    case 2: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
-    case 4: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
-    default: return launch_scan<T, kTile<T, VEC>, 2, scan_fwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
-  }
+  return with_cluster(
+      d, kTile<T, VEC>,
+      [](auto CL) { return resident<T, 2, CL(), scan_fwd_kernel<T, VEC, CL(), stages_of(2)>>(); },
+      [&](auto CL) {
+        return launch_scan<T, kTile<T, VEC>, 2, CL(), scan_fwd_kernel<T, VEC, CL(), stages_of(2)>>(d, st, d, args...);
+      });
 }
 
 template <typename T, bool VEC, typename... A>
 int scan_bwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
-  constexpr int S = stages_of(3);
-  switch (cluster_of(d, kTile<T, VEC>)) {
-    case 1: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 1, S>>(d, 1, st, d, args...);
-    case 2: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 2, S>>(d, 2, st, d, args...);
-    case 4: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 4, S>>(d, 4, st, d, args...);
-    default: return launch_scan<T, kTile<T, VEC>, 3, scan_bwd_kernel<T, VEC, 8, S>>(d, 8, st, d, args...);
-  }
+  return with_cluster(
+      d, kTile<T, VEC>,
+      [](auto CL) { return resident<T, 3, CL(), scan_bwd_kernel<T, VEC, CL(), stages_of(3)>>(); },
+      [&](auto CL) {
+        return launch_scan<T, kTile<T, VEC>, 3, CL(), scan_bwd_kernel<T, VEC, CL(), stages_of(3)>>(d, st, d, args...);
+      });
 }
 
 template <typename T>
