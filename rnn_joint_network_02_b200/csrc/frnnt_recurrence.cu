@@ -20,7 +20,6 @@ namespace {
 constexpr int kChunk = FRNNT_SCAN_CHUNK;
 constexpr int kSteps = 16;
 constexpr int kWarps = kChunk / kSteps;
-static_assert(kWarps >= 8, "a warp for each block of a cluster");
 
 // a = sigmoid(gate) and s = 1 - a = sigmoid(-gate), each to relative precision:
 // with e = exp(-gate), a = 1 / (1 + e), and s = e a where that is below 1/2 (1 -
@@ -587,6 +586,7 @@ int resident() {
   if (const int n = here.load(std::memory_order_acquire)) return n - 1;
   constexpr int bytes = kMostBytes<T, ARRAYS>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -1;
+  if (CL > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
   int n = INT_MAX - 1;
   if (CL > 1) {
     cudaLaunchAttribute size;
@@ -606,9 +606,10 @@ int resident() {
 }
 
 // Blocks that share a sequence's chunks: as few as give the fewest rounds, of
-// those whose clusters run all at once.  (Clusters of 6 are why 8 x 1500 x 513
-// bf16 takes 17 us and 27 us backward: 23 and 38 with 4; but 3 x 10000 x 1024,
-// whose 48 do not all fit, 61 us and 94 with 6, 55 and 85 with 4.)
+// those whose clusters run all at once.  bf16, forward and backward, with 8 at
+// most and powers of two only: 8 x 1500 x 513 23 us and 38, here (6) 17 and 27; 1 x
+// 32749 x 64 61 and 91, here (16) 37 and 50.  Clusters that do not all fit: 3 x
+// 10000 x 1024 61 and 94 (48 of 6), here (5) 44 and 68.
 template <typename Fit, typename Launch>
 int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launch) {
   const long long tiles = (long long)((d.D + tile - 1) / tile) * d.B;
@@ -625,6 +626,8 @@ int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launc
   may(integral_constant<int, 5>());
   may(integral_constant<int, 6>());
   may(integral_constant<int, 8>());
+  may(integral_constant<int, 10>());
+  may(integral_constant<int, 16>());
   switch (best) {
     case 1: return launch(integral_constant<int, 1>());
     case 2: return launch(integral_constant<int, 2>());
@@ -632,7 +635,9 @@ int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launc
     case 4: return launch(integral_constant<int, 4>());
     case 5: return launch(integral_constant<int, 5>());
     case 6: return launch(integral_constant<int, 6>());
-    default: return launch(integral_constant<int, 8>());
+    case 8: return launch(integral_constant<int, 8>());
+    case 10: return launch(integral_constant<int, 10>());
+    default: return launch(integral_constant<int, 16>());
   }
 }
 

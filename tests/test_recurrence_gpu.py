@@ -249,3 +249,28 @@ def test_step_bad_parent_raises(cuda_ok):
         with pytest.raises(frnnt.FrnntStatusError) as e:
             frnnt.recurrence_step(x, x, state, parent=parent)
         assert e.value.bits == frnnt.STATUS_INDEX
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["plain", "offset"])
+@pytest.mark.parametrize("B,T,D", [(1, 200, 64), (3, 300, 34), (2, 600, 128), (1, 700, 64), (1, 1280, 70), (1, 4200, 64),
+                                   (40, 1300, 128), (50, 700, 120), (30, 2100, 66), (60, 1000, 64)])
+def test_cluster_sizes(cuda_ok, B, T, D, layout, dtype):
+    """Chunk and tile counts that take each number of blocks a sequence, for one
+    round and for several, the last one not full."""
+    check(*make(B, T, D, dtype, layout, seed=9), dtype)
+
+
+def test_few_and_many_sequences_agree(cuda_ok):
+    """The blocks that share a sequence depend on the batch; the states they form agree to their rounding."""
+    x, gate, _, h0, dh, dl = make(64, 900, 64, "f32", ragged=False, seed=10)
+    many = frnnt.recurrence(x, gate, h0=h0)
+    dm = frnnt.recurrence_bwd(x, gate, many, dh, dh_last=dl)
+    ref = O.recurrence(host(x[:1]), host(gate[:1]), None, host(h0[:1]), "f32")
+    want = O.recurrence_bwd(host(x[:1]), host(gate[:1]), ref, host(dh[:1]), None, host(dl[:1]), "f32")
+    one = frnnt.recurrence(x[:1], gate[:1], h0=h0[:1])
+    do = frnnt.recurrence_bwd(x[:1], gate[:1], one, dh[:1], dh_last=dl[:1])
+    for r, d in ((many, dm), (one, do)):
+        close(r.h[:1], ref["h"], ref["h_tol"], "h")
+        for k in ("dx", "dgate", "dh0"):
+            close(d[k][:1], want[k], want[k + "_tol"], k)
