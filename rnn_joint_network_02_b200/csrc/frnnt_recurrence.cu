@@ -625,6 +625,7 @@ int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launc
   may(integral_constant<int, 4>());
   may(integral_constant<int, 5>());
   may(integral_constant<int, 6>());
+  may(integral_constant<int, 7>());
   may(integral_constant<int, 8>());
   may(integral_constant<int, 10>());
   may(integral_constant<int, 16>());
@@ -635,6 +636,7 @@ int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launc
     case 4: return launch(integral_constant<int, 4>());
     case 5: return launch(integral_constant<int, 5>());
     case 6: return launch(integral_constant<int, 6>());
+    case 7: return launch(integral_constant<int, 7>());
     case 8: return launch(integral_constant<int, 8>());
     case 10: return launch(integral_constant<int, 10>());
     default: return launch(integral_constant<int, 16>());

@@ -253,7 +253,7 @@ def test_step_bad_parent_raises(cuda_ok):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["plain", "offset"])
-@pytest.mark.parametrize("B,T,D", [(1, 200, 64), (3, 300, 34), (2, 600, 128), (1, 700, 64), (1, 1280, 70), (1, 4200, 64),
+@pytest.mark.parametrize("B,T,D", [(1, 200, 64), (3, 300, 34), (2, 600, 128), (1, 700, 64), (1, 800, 64), (1, 1280, 70), (1, 4200, 64),
                                    (40, 1300, 128), (50, 700, 120), (30, 2100, 66), (60, 1000, 64)])
 def test_cluster_sizes(cuda_ok, B, T, D, layout, dtype):
     """Chunk and tile counts that take each number of blocks a sequence, for one
