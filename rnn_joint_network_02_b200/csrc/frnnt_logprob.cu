@@ -980,10 +980,10 @@ __global__ void __launch_bounds__(kWarps * 32, SKEW && sizeof(T) == 2 ? 2 : 3)
 // Short rows: G lanes a row, as in the forward pass.  Every lane goes through the
 // row's coefficients and adds up those of its own columns, so no column is
 // written twice and every element is read and written by one lane (dlogits may be
-// the logits' memory).  60000 x 128 bf16, two tokens and the entropy: 18.4 us, x
-// 24: 4.7 us.
+// the logits' memory).  Bound by latency: five blocks an SM, 60000 x 128 bf16, two
+// tokens and the entropy: 16.0 us (four: 18.3, six: 16.7), x 24: 4.6.
 template <typename T, int G, int C>
-__global__ void __launch_bounds__(kWarps * 32) logprob_bwd_few_kernel(BwdParams p, const T* logits, T* dlogits) {
+__global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdParams p, const T* logits, T* dlogits) {
   const int lane = threadIdx.x & 31, g = lane % G;
   const long long n = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / G) + lane / G;
   if (n >= p.N) return;   // (no lane waits for another)
@@ -1128,9 +1128,9 @@ bool with_few_top(int V, Go go) {
   if (V <= 128) return take<32, 4>(go);
   return V <= 256 && take<32, 8>(go);
 }
-// The gradient, whose every lane goes through all coefficients.  2 of them, 24 / 64 / 128 / 256 logits: 4.7 / 9.5 /
-// 18.4 / 33 us here (256 with 16 columns a lane), 21 / 21 / 23 / 24 in logprob_bwd_rows_kernel; 8 of them, 64 / 128: 15
-// / 27 here, 38 / 41 in logprob_bwd_kernel; 24 of them: 29 / 55 and 48 / 49
+// The gradient, whose every lane goes through all coefficients.  2 of them, 24 / 64 / 128 / 256 logits: 4.6 / 8.0 /
+// 16 / 33 us here (256 with 16 columns a lane), 21 / 21 / 23 / 24 in logprob_bwd_rows_kernel; 8 of them, 64 / 128: 14 /
+// 25 here, 38 / 41 in logprob_bwd_kernel; 24 of them: 29 / 55 and 48 / 49
 template <typename Go>
 bool with_few_bwd(int V, int slots, Go go) {
   if (V <= 16) return take<2, 8>(go);
