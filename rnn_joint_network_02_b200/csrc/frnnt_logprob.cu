@@ -378,8 +378,8 @@ __device__ __forceinline__ void write_stats(const FwdParams& p, long long n, con
   p.lse[n] = empty ? -INFINITY : st.m + ls;
   p.entropy[n] = empty ? 0.f : fmaf(st.w / st.s, -kLn2, ls);
 }
-__device__ __forceinline__ void write_token(const FwdParams& p, long long n, int k, const Stats& st, float ls, int token,
-                                            float z) {
+__device__ __forceinline__ void write_token(const FwdParams& p, long long n, int k, const Stats& st, float ls,
+                                            int token, float z) {
   const bool given = token >= 0 && token < p.V;
   if (!given && token != FRNNT_NO_TOKEN && p.status) atomicOr(p.status, FRNNT_STATUS_LABEL);
   p.logp[n * p.K + k] = !given ? 0.f : st.s == 0.f ? -INFINITY : (z - st.m) - ls;
@@ -457,7 +457,8 @@ struct Share {
 // values of their first tokens are fetched before the rows are scanned.
 constexpr int kEarly = 2;
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kWarps * 32, 3) logprob_warp_kernel(FwdParams p, uint64_t step, const T* __restrict__ logits) {
+__global__ void __launch_bounds__(kWarps * 32, 3)
+    logprob_warp_kernel(FwdParams p, uint64_t step, const T* __restrict__ logits) {
   using Order = std::conditional_t<sizeof(T) == 2, Narrow, Wide>;   // (its rows are shorter than 65535)
   __shared__ __align__(16) unsigned char waiting[TOP ? kWarps : 1][kWaitingBytes];
   __shared__ int counts[kWarps];
@@ -1215,8 +1216,8 @@ void launch_bwd(BwdParams p, const T* logits, T* dlogits, cudaStream_t st) {
 
 int check(const frnnt_logprob_dims* d) {
   if (d->dtype != FRNNT_F32 && d->dtype != FRNNT_BF16) return FRNNT_ERR_UNSUPPORTED;
-  if (d->N < 1 || d->N > (1 << 27) || d->V < 1 || d->V > (1 << 30) || d->K < 0 || d->K > FRNNT_MAX_TOKENS || d->top < 0 || d->top > FRNNT_MAX_TOP ||
-      d->top > d->V || d->ld < d->V || d->ld > (1LL << 40))
+  if (d->N < 1 || d->N > (1 << 27) || d->V < 1 || d->V > (1 << 30) || d->K < 0 || d->K > FRNNT_MAX_TOKENS ||
+      d->top < 0 || d->top > FRNNT_MAX_TOP || d->top > d->V || d->ld < d->V || d->ld > (1LL << 40))
     return FRNNT_ERR_DIMS;
   return FRNNT_OK;
 }
@@ -1273,8 +1274,8 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs_bwd", st);
-    const BwdParams p{d->N, d->V, d->K, d->top, 1, 0, d->ld, d->ldd, tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,
-                      status};
+    const BwdParams p{d->N, d->V, d->K,    d->top, 1,     0,        d->ld, d->ldd,
+                      tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,  status};
     if (d->dtype == FRNNT_BF16) launch_bwd(p, (const __nv_bfloat16*)logits, (__nv_bfloat16*)dlogits, st);
     else launch_bwd(p, (const float*)logits, (float*)dlogits, st);
   }

@@ -586,7 +586,8 @@ int resident() {
   if (const int n = here.load(std::memory_order_acquire)) return n - 1;
   constexpr int bytes = kMostBytes<T, ARRAYS>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -1;
-  if (CL > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
+  if (CL > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return -1;
   int n = INT_MAX - 1;
   if (CL > 1) {
     cudaLaunchAttribute size;
@@ -650,7 +651,8 @@ int launch_scan(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
   const dim3 grid((d.D + TILE - 1) / TILE * CL, d.B);
   // one round needs one chunk's memory, and a short one only its rows
   const int rounds = ((d.T + kChunk - 1) / kChunk + CL - 1) / CL;
-  const int bytes = rounds >= stages_of(ARRAYS) ? kMostBytes<T, ARRAYS> : rounds * (int)sizeof(Stage<T>) * ARRAYS + kSlack;
+  const int bytes =
+      rounds >= stages_of(ARRAYS) ? kMostBytes<T, ARRAYS> : rounds * (int)sizeof(Stage<T>) * ARRAYS + kSlack;
   launch_k(kernel, grid, dim3(warps * 32), bytes, st, CL, args...);
   note_launch();
   return FRNNT_OK;

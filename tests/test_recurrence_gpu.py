@@ -2,7 +2,10 @@
 backward and the one-step form, over types, lengths (zero, one, long, ragged),
 odd sizes and strides."""
 
+import subprocess
+import sys
 import threading
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -274,3 +277,28 @@ def test_few_and_many_sequences_agree(cuda_ok):
         close(r.h[:1], ref["h"], ref["h_tol"], "h")
         for k in ("dx", "dgate", "dh0"):
             close(d[k][:1], want[k], want[k + "_tol"], k)
+
+
+FIRST_CALL = """
+import torch
+from rnn_joint_network_02_b200 import frnnt
+x, gate = (torch.randn(1, 1500, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+dh = torch.randn_like(x)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r = frnnt.recurrence(x, gate, check=False)
+    d = frnnt.recurrence_bwd(x, gate, r, dh, check=False)
+graph.replay()
+want = frnnt.recurrence(x, gate)
+grads = frnnt.recurrence_bwd(x, gate, want, dh)
+assert torch.equal(r.h, want.h) and all(torch.equal(d[k], grads[k]) for k in grads)
+print("same")
+"""
+
+
+def test_first_call_of_a_process_is_captured(cuda_ok):
+    """What a kernel asks of the runtime once may be asked during a capture."""
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
+                          cwd=Path(__file__).resolve().parent.parent)
+    assert done.returncode == 0 and done.stdout.strip().endswith("same"), done.stderr[-2000:]
