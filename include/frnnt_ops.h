@@ -17,7 +17,8 @@
  *   - `status` may be NULL.  When given, invalid device-side values OR their FRNNT_STATUS_* bits into it: the
  *     call never clears it, the caller does.  After a bit was set the outputs of the rows concerned are
  *     unspecified; no access out of bounds happens either way.  FRNNT_STATUS_TIMEOUT: a bounded wait of the
- *     recurrence's blocks for each other gave up.
+ *     recurrence's blocks for each other gave up (after about 2 s; the call then ends within a few seconds, and
+ *     later calls are not concerned).
  * Outputs must not overlap inputs except where a call says so.
  */
 #ifndef FRNNT_OPS_H

@@ -48,6 +48,21 @@ FRNNT_API int frnnt_test_joint_variant(int variant);
  * (set it between calls).  Returns the previous count. */
 FRNNT_API int frnnt_test_lose_gemm_loads(int n);
 
+/* Failure-detection test setting of the recurrence: in each of the next n
+ * launches of frnnt_recurrence_fwd / _bwd whose sequences are shared by a
+ * cluster of blocks, block 0 of every cluster withholds the message of one
+ * round (quit = 0), so that every block's bounded wait in that round runs out;
+ * or (quit = 1) sends it and gives up at once, so that the others' waits run
+ * out in the next round, if there is one.  `round` counts from a sequence's
+ * first round, or, when negative, from its last (-1); `tries` replaces the
+ * waits' limit (polls of 0.1 ms, 20000 at most).  Every block of the cluster
+ * then stops, waits (with the same limit) for the messages that were sent to
+ * it, and FRNNT_STATUS_TIMEOUT is ORed into the call's status word (when one is
+ * given); those sequences' outputs are left incomplete, and later calls run
+ * normally.  n <= 0 clears the setting.  Process-wide, not thread-safe (set it
+ * between calls).  Returns the launches that were still to come. */
+FRNNT_API int frnnt_test_lose_scan_maps(int n, int round, int quit, int tries);
+
 /* The K-slice count the tensor-core GEMM takes for a split-K launch (host
  * only, no GPU needed): mn output tiles on `workers` persistent CTAs (or CTA
  * pairs), kblocks K blocks of 64.  It minimises rounds x (K blocks per unit +

@@ -190,24 +190,44 @@ __device__ __forceinline__ Map map_one() { return Map{f2_of(1.f, 1.f), f2_of(0.f
 __device__ __forceinline__ Map then(Map f, Map g) { return Map{f2_mul(g.A, f.A), f2_fma(g.A, f.R, g.R)}; }
 __device__ __forceinline__ uint64_t apply(Map f, uint64_t v) { return f2_fma(f.A, v, f.R); }
 
+// A launch in which the exchange below fails on purpose (frnnt_test_lose_scan_maps): block 0 of every cluster, in one
+// round (counted from the last when negative), sends no map (kLose), or sends it and gives up without waiting (kQuit).
+struct Trial {
+  enum { kNone, kLose, kQuit };
+  int kind = kNone, round = 0;
+  uint32_t tries = sm100::kMaxTries;   // polls of a wait
+  __device__ __forceinline__ bool here(int what, int r, int rank, int rounds) const {
+    return kind == what && rank == 0 && r == (round < 0 ? rounds + round : round);
+  }
+};
+
 // The blocks of a cluster tell each other the map of their chunk: the first warp
 // of every block sends it to every block's shared memory, where an mbarrier
 // counts the bytes of all CL maps.  Two buffers: a warp that sends round r + 2
 // has received round r + 1 from all, and each sent that after it had read round r.
+// A wait that runs out ends the block: it neither sends nor arrives again, so the
+// others' waits run out a round later at the latest, and it leaves when no map
+// can still come (see leave).
 template <int CL>
 struct Exchange {
+  static constexpr uint32_t kBytes = 32 * sizeof(ulonglong2);   // of a map
   ulonglong2 maps[2][CL][32];
   uint64_t full[2];
+  int gave_up;    // 1 + the round whose wait ran out, 0: none
+  int sent[CL];   // rounds that a block sent which gave up before its last one (else: all)
 
   __device__ __forceinline__ void init() {
     if (threadIdx.x == 0) {
       sm100::mbar_init(&full[0], 1);
       sm100::mbar_init(&full[1], 1);
       sm100::fence_barrier_init();
+      gave_up = 0;
     }
+    if (threadIdx.x < CL) sent[threadIdx.x] = INT_MAX;
   }
-  __device__ __forceinline__ void send(int r, int rank, int lane, Map m) {
-    if (lane == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * 32 * sizeof(ulonglong2));
+  __device__ __forceinline__ void send(int r, int rank, int rounds, int lane, Map m, const Trial& trial) {
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * kBytes);
+    if (trial.here(Trial::kLose, r, rank, rounds)) return;
 #pragma unroll
     for (int k = 0; k < CL; ++k)
       asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
@@ -215,18 +235,60 @@ struct Exchange {
                    "l"(m.A), "l"(m.R), "r"(in_cluster(&full[r & 1], k))
                    : "memory");
   }
-  // The carry after this round; `in`: what enters block `rank`'s chunk.
-  __device__ __forceinline__ uint64_t receive(int r, int rank, int lane, uint64_t carry, uint64_t& in, int32_t* status) {
+  __device__ __forceinline__ bool wait(int r, uint32_t tries) {
     bool ok = sm100::mbar_try_wait_cluster(&full[r & 1], (r >> 1) & 1, 0);
-    for (uint32_t i = 0; !ok && i < sm100::kMaxTries; ++i)
+    for (uint32_t i = 0; !ok && i < tries; ++i)
       ok = sm100::mbar_try_wait_cluster(&full[r & 1], (r >> 1) & 1, sm100::kSuspendNs);
-    if (!ok && status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
+    return ok;
+  }
+  // The carry after this round; `in`: what enters block `rank`'s chunk.  When the
+  // wait runs out (for all lanes alike), gave_up is set and the carry means nothing.
+  __device__ __forceinline__ uint64_t receive(int r, int rank, int rounds, int lane, uint64_t carry, uint64_t& in,
+                                              const Trial& trial, int32_t* status) {
+    const bool ok = !trial.here(Trial::kQuit, r, rank, rounds) && wait(r, trial.tries);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) {
+        gave_up = r + 1;
+        if (status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
+      }
+      return carry;
+    }
     for (int k = 0; k < CL; ++k) {
       if (k == rank) in = carry;
       const ulonglong2 o = maps[r & 1][k][lane];
       carry = f2_fma(o.x, carry, o.y);
     }
     return carry;
+  }
+  // The end of a block that gave up in round r, which it sent.  Maps of rounds r
+  // and r + 1 may still be on their way to it (r + 2 needs its r + 1).  Every
+  // block of the cluster gives up too or has left after its last round, so all
+  // of them meet here or are gone; what each sent is known then, and the bytes
+  // of that are awaited.  While this block has a round to send, no block can
+  // have received all rounds and left, so the count may be told to each.
+  __device__ __noinline__ void leave(int rank, int rounds, uint32_t tries) {
+    const int r = gave_up - 1;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (threadIdx.x < CL && r + 1 < rounds)
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(in_cluster(&sent[rank], threadIdx.x)), "r"(r + 1)
+                   : "memory");
+    cluster_arrive();
+    cluster_wait();   // (for the threads that have not exited)
+    if (threadIdx.x != 0) return;
+    uint32_t missing = 0, ahead = 0;
+    for (int k = 0; k < CL; ++k) {
+      missing += sent[k] <= r;
+      ahead += r + 1 < rounds && sent[k] > r + 1;
+    }
+    if (missing)   // the arrival in send() expects the bytes of all
+      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(&full[r & 1])),
+                   "r"(missing * kBytes)
+                   : "memory");
+    wait(r, tries);
+    if (ahead) {
+      sm100::mbar_arrive_expect_tx(&full[(r + 1) & 1], ahead * kBytes);
+      wait(r + 1, tries);
+    }
   }
 };
 template <>
@@ -252,7 +314,7 @@ template <typename T, bool VEC, int CL, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     scan_fwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ h0, T* __restrict__ h,
-                    float* __restrict__ h_last, float* __restrict__ saved, int32_t* status) {
+                    float* __restrict__ h_last, float* __restrict__ saved, int32_t* status, Trial trial) {
   extern __shared__ __align__(128) unsigned char smem[];
   Stage<T>* stage = reinterpret_cast<Stage<T>*>(smem);   // [STAGES][x, gate]
   __shared__ ulonglong2 run[kWarps][32];
@@ -303,8 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL > 1) {
         Map all = map_one();
         for (int k = 0; k < nw; ++k) all = then(all, Map{run[k][lane].x, run[k][lane].y});
-        ex.send(r, rank, lane, all);
-        carry = ex.receive(r, rank, lane, carry, in, status);
+        ex.send(r, rank, rounds, lane, all, trial);
+        carry = ex.receive(r, rank, rounds, lane, carry, in, trial, status);
       }
       if (t0 < len) store_state<kApart<T, VEC>>(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
       for (int k = 0; k < nw; ++k) {
@@ -315,6 +377,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL == 1) carry = in;
     }
     __syncthreads();
+    if constexpr (CL > 1)
+      if (ex.gave_up) break;
     uint64_t s = run[w][lane].y;
     if (VEC && whole && t0 + kSteps <= len) {
       char* base = reinterpret_cast<char*>(h + b * d.h_sb + c0 + (long long)(r * CL + rank) * kChunk * d.h_st);
@@ -346,6 +410,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
     if (live) store_pair<T, VEC>(hp + t * d.h_st, make_float2(0.f, 0.f), two);
   if (rank == 0 && w == 0) store_state<kApart<T, VEC>>(h_last, b, d.D, c, live, two, carry);
+  if constexpr (CL > 1)
+    if (rounds && ex.gave_up) ex.leave(rank, rounds, trial.tries);
 }
 
 // Backward.  With q_t = a_t g_t, what step t hands to step t - 1, q_t = a_t
@@ -360,7 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     scan_bwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
                     const int32_t* __restrict__ lengths, const float* __restrict__ saved, const T* __restrict__ dh,
                     const float* __restrict__ dh_last, T* __restrict__ dx, T* __restrict__ dgate,
-                    float* __restrict__ dh0, int32_t* status) {
+                    float* __restrict__ dh0, int32_t* status, Trial trial) {
   extern __shared__ __align__(128) unsigned char smem[];
   Stage<T>* stage = reinterpret_cast<Stage<T>*>(smem);   // [STAGES][x, gate, dh]
   __shared__ ulonglong2 run[kWarps][32];   // forward maps
@@ -424,14 +490,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL > 1) {
         Map all = map_one();
         for (int k = nw - 1; k >= 0; --k) all = then(all, Map{run[k][lane].x, back[k][lane]});
-        ex.send(r, rank, lane, all);
+        ex.send(r, rank, rounds, lane, all, trial);
       }
       for (int k = 0; k < nw; ++k) {
         const ulonglong2 o = run[k][lane];
         run[k][lane].y = v;
         v = apply(Map{o.x, o.y}, v);
       }
-      if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, status);
+      if constexpr (CL > 1) carry = ex.receive(r, rank, rounds, lane, carry, in, trial, status);
       for (int k = nw - 1; k >= 0; --k) {
         const uint64_t o = back[k][lane];
         back[k][lane] = in;
@@ -440,6 +506,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL == 1) carry = in;
     }
     __syncthreads();
+    if constexpr (CL > 1)
+      if (ex.gave_up) break;
     v = run[w][lane].y;
     q = back[w][lane];
 #pragma unroll
@@ -496,6 +564,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       store_pair<T, VEC>(dgp + t * d.dgate_st, make_float2(0.f, 0.f), two);
     }
   if (rank == 0 && w == 0) store_state<kApart<T, VEC>>(dh0, b, d.D, c, live, two, carry);
+  if constexpr (CL > 1)
+    if (rounds && ex.gave_up) ex.leave(rank, rounds, trial.tries);
 }
 
 // One step: a thread takes C neighbouring channels of a row in one access an
@@ -658,6 +728,16 @@ int launch_scan(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
   return FRNNT_OK;
 }
 
+// The trial that the next launch makes (see frnnt_test_lose_scan_maps).
+int g_trials = 0;
+Trial g_trial;
+template <int CL>
+Trial trial_of() {
+  if (CL == 1 || g_trials == 0) return Trial();
+  --g_trials;
+  return g_trial;
+}
+
 // Rows of 16-byte vectors throughout, and chunks that 32-bit offsets span.
 bool vectors_ok(const frnnt_recurrence_dims& d, std::initializer_list<const void*> ptrs,
                 std::initializer_list<long long> seqs, std::initializer_list<long long> steps) {
@@ -677,7 +757,8 @@ int scan_fwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
       d, kTile<T, VEC>,
       [](auto CL) { return resident<T, 2, CL(), scan_fwd_kernel<T, VEC, CL(), stages_of(2)>>(); },
       [&](auto CL) {
-        return launch_scan<T, kTile<T, VEC>, 2, CL(), scan_fwd_kernel<T, VEC, CL(), stages_of(2)>>(d, st, d, args...);
+        return launch_scan<T, kTile<T, VEC>, 2, CL(), scan_fwd_kernel<T, VEC, CL(), stages_of(2)>>(d, st, d, args...,
+                                                                                                   trial_of<CL()>());
       });
 }
 
@@ -687,7 +768,8 @@ int scan_bwd(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
       d, kTile<T, VEC>,
       [](auto CL) { return resident<T, 3, CL(), scan_bwd_kernel<T, VEC, CL(), stages_of(3)>>(); },
       [&](auto CL) {
-        return launch_scan<T, kTile<T, VEC>, 3, CL(), scan_bwd_kernel<T, VEC, CL(), stages_of(3)>>(d, st, d, args...);
+        return launch_scan<T, kTile<T, VEC>, 3, CL(), scan_bwd_kernel<T, VEC, CL(), stages_of(3)>>(d, st, d, args...,
+                                                                                                   trial_of<CL()>());
       });
 }
 
@@ -710,6 +792,16 @@ int bwd_of(bool vec, const frnnt_recurrence_dims& d, const void* x, const void* 
 }
 
 }  // namespace
+
+int lose_scan_maps(int n, int round, bool quit, int tries) {
+  const int prev = g_trials;
+  g_trials = n < 0 ? 0 : n;
+  g_trial.kind = quit ? Trial::kQuit : Trial::kLose;
+  g_trial.round = round;
+  g_trial.tries = tries < 0 ? 0u : tries < (int)sm100::kMaxTries ? (uint32_t)tries : sm100::kMaxTries;
+  return prev;
+}
+
 }  // namespace frnnt
 
 using namespace frnnt;

@@ -33,6 +33,10 @@ extern "C" FRNNT_API int frnnt_test_joint_variant(int variant) { return frnnt::s
 
 extern "C" FRNNT_API int frnnt_test_lose_gemm_loads(int n) { return frnnt::lose_gemm_loads(n); }
 
+extern "C" FRNNT_API int frnnt_test_lose_scan_maps(int n, int round, int quit, int tries) {
+  return frnnt::lose_scan_maps(n, round, quit != 0, tries);
+}
+
 extern "C" FRNNT_API int frnnt_test_auto_splits(int mn, int workers, int kblocks) {
   return frnnt::auto_splits(mn, workers, kblocks);
 }

@@ -31,7 +31,8 @@ EXPORTED = ("frnnt_workspace_size", "frnnt_fwd_bwd", "frnnt_error_string", "frnn
 MAX_DURATIONS = 8
 MAX_TOKENS, MAX_TOP, NO_TOKEN, SCAN_CHUNK = 32, 32, -1, 128
 NOALLOC_MAX_BYTES = 64 * 1024 * 1024
-TEST_HOOKS = ("frnnt_test_gemm_bf16", "frnnt_test_joint_variant", "frnnt_test_lose_gemm_loads")
+TEST_HOOKS = ("frnnt_test_gemm_bf16", "frnnt_test_joint_variant", "frnnt_test_lose_gemm_loads",
+              "frnnt_test_lose_scan_maps")
 
 
 class Dims(ctypes.Structure):
@@ -135,6 +136,8 @@ def lib() -> ctypes.CDLL:
         L.frnnt_test_joint_variant.restype = ctypes.c_int
         L.frnnt_test_lose_gemm_loads.argtypes = [ctypes.c_int]
         L.frnnt_test_lose_gemm_loads.restype = ctypes.c_int
+        L.frnnt_test_lose_scan_maps.argtypes = [ctypes.c_int] * 4
+        L.frnnt_test_lose_scan_maps.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -421,6 +424,14 @@ def lose_gemm_loads(n: int) -> int:
     launches drop their first K block load, so their bounded wait runs out and
     the status word gets STATUS_TIMEOUT.  Returns the previous count."""
     return int(lib().frnnt_test_lose_gemm_loads(int(n)))
+
+
+def lose_scan_maps(n: int, round: int = 0, quit: bool = False, tries: int = 200) -> int:
+    """Test setting (include/frnnt_testing.h): in the next n recurrence launches
+    with clusters of blocks, one block of each withholds its message of a round
+    (or gives up after it), so bounded waits run out and the status word gets
+    STATUS_TIMEOUT.  Returns the launches that were still to come."""
+    return int(lib().frnnt_test_lose_scan_maps(int(n), int(round), int(quit), int(tries)))
 
 
 def set_joint_variant(variant: int) -> int:

@@ -1,0 +1,78 @@
+"""Failure detection in the recurrence, without a fault: a message between the
+blocks that share a sequence is withheld, or a block gives up (the
+lose_scan_maps test setting), so bounded waits run out.  The call must end soon,
+report FRNNT_STATUS_TIMEOUT, leave the sequences that had no part in it right,
+and leave the context usable: the same calls made again give the same bits as
+before."""
+
+import time
+
+import pytest
+import torch
+
+from rnn_joint_network_02_b200 import frnnt
+from tests.test_recurrence_gpu import make
+
+pytestmark = pytest.mark.gpu
+KEYS = ("dx", "dgate", "dh0")
+
+
+@pytest.fixture
+def lose_maps():
+    frnnt.lose_scan_maps(0)
+    yield frnnt.lose_scan_maps
+    frnnt.lose_scan_maps(0)
+
+
+def _times_out(call):
+    start = time.monotonic()
+    with pytest.raises(frnnt.FrnntStatusError) as e:
+        call()
+    torch.cuda.synchronize()
+    assert e.value.bits == frnnt.STATUS_TIMEOUT
+    assert frnnt.lose_scan_maps(0) == 0, "the setting is consumed by exactly one launch"
+    return time.monotonic() - start
+
+
+# sequences, steps, channels that clusters of blocks share, in one round (the first) or three and more
+SHAPES = [(3, 300, 34, "plain", "bf16"), (1, 4200, 64, "plain", "bf16"), (30, 2100, 66, "plain", "bf16"),
+          (40, 1300, 128, "plain", "bf16"), (3, 300, 34, "offset", "f32"), (1, 4200, 64, "offset", "f32"),
+          (30, 2100, 66, "offset", "f32"), (30, 1300, 64, "offset", "f32")]
+
+
+@pytest.mark.parametrize("quit", [False, True])
+@pytest.mark.parametrize("round", [0, 1, 2, -1])
+@pytest.mark.parametrize("B,T,D,layout,dtype", SHAPES)
+def test_lost_map_times_out_and_context_survives(cuda_ok, lose_maps, B, T, D, layout, dtype, round, quit):
+    if round > 0 and T < 1000:
+        pytest.skip("one round only")
+    x, gate, lengths, h0, dh, dl = make(B, T, D, dtype, layout, seed=51)
+    r = frnnt.recurrence(x, gate, lengths=lengths, h0=h0)
+    d = frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)
+    want = [t.clone() for t in (r.h, r.h_last, *(d[k] for k in KEYS))]
+
+    lose_maps(1, round, quit)
+    assert _times_out(lambda: frnnt.recurrence(x, gate, lengths=lengths, h0=h0)) < 5
+    lose_maps(1, round, quit)
+    assert _times_out(lambda: frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)) < 5
+
+    # sequences without such a round (here: empty ones, and of one step where a later round is meant) take no harm
+    lose_maps(1, round, quit)
+    hurt = frnnt.recurrence(x, gate, lengths=lengths, h0=h0, check=False)
+    short = [b for b, n in enumerate(lengths.tolist()) if n == 0 or (n == 1 and round > 0)]
+    assert all(torch.equal(hurt.h[b], want[0][b]) and torch.equal(hurt.h_last[b], want[1][b]) for b in short)
+
+    r = frnnt.recurrence(x, gate, lengths=lengths, h0=h0)
+    d = frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)
+    assert all(torch.equal(a, b) for a, b in zip((r.h, r.h_last, *(d[k] for k in KEYS)), want))
+
+
+def test_the_limit_itself(cuda_ok, lose_maps):
+    """With the limit of ordinary calls (2 s a wait): the first wait in a round of many, each block's second one for
+    what is on its way to it, and nothing else."""
+    x, gate, _, _, _, _ = make(1, 20000, 64, "bf16", ragged=False, seed=52)
+    want = frnnt.recurrence(x, gate).h.clone()
+    lose_maps(1, 2, False, 20000)
+    took = _times_out(lambda: frnnt.recurrence(x, gate))
+    assert took < 15, took
+    assert torch.equal(frnnt.recurrence(x, gate).h, want)
