@@ -318,16 +318,26 @@ class Dropout(NamedTuple):
         return (f.numel() + 7) // 8 + (g.numel() + 7) // 8
 
 
-def _with_dropout(drop, f, g, out, stream, call):
-    """``call(f, g)`` on the dropped inputs, its df and dg masked alike."""
+def _with_dropout(drop, f, g, out, call):
+    """``call(f, g)`` on the dropped inputs, its df and dg masked alike, all on the current stream."""
     if out is not None and out.dropped is None:
         out.dropped = (torch.empty_like(f), torch.empty_like(g))
     fd, gd = (None, None) if out is None else out.dropped
     at = (drop.offset, drop.offset + (f.numel() + 7) // 8)
-    loss, grads = call(dropout(f, drop.p, drop.seed, at[0], fd, stream), dropout(g, drop.p, drop.seed, at[1], gd, stream))
-    dropout(grads["df"], drop.p, drop.seed, at[0], grads["df"], stream)
-    dropout(grads["dg"], drop.p, drop.seed, at[1], grads["dg"], stream)
+    loss, grads = call(dropout(f, drop.p, drop.seed, at[0], fd), dropout(g, drop.p, drop.seed, at[1], gd))
+    dropout(grads["df"], drop.p, drop.seed, at[0], grads["df"])
+    dropout(grads["dg"], drop.p, drop.seed, at[1], grads["dg"])
     return loss, grads
+
+
+def _loss_place(dev, stream):
+    """The context that a loss call is made in (see _elsewhere), so that the
+    buffers it allocates belong to its stream and its status is read there; None
+    where the stream that is given is the current one."""
+    if stream is not None and _raw_stream and stream.device == dev and _current_device() == dev.index and \
+            stream.cuda_stream == _raw_stream(dev.index):
+        return None
+    return _elsewhere(dev, stream)
 
 
 def fwd_bwd(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=None, mode="tiled", path="auto",
@@ -339,26 +349,31 @@ def fwd_bwd(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=None, mode
     ``loss`` is "marginal" (every alignment) or "viterbi" (the best one).
     ``wgrad_f32``: the weight gradients come back in fp32 (unrounded).
     ``dropout``: of f and g, see Dropout.
+    ``stream``: the work is queued there instead of on the current stream, and
+    what the call allocates belongs to it.
     Returns (loss [B] fp32, dict of gradients).  With ``check`` the device
     status word is read back (one 4-byte device-to-host copy, which
     synchronises the stream) and a non-zero status raises FrnntStatusError.
     """
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, wgrad_f32=wgrad_f32)
+    there = _loss_place(f.device, stream)
+    if there is not None:
+        with there:
+            return fwd_bwd(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells, blank,
+                           out, check, None, loss, wgrad_f32, dropout)
     if dropout is not None:
-        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd(
+        return _with_dropout(dropout, f, g, out, lambda f, g: fwd_bwd(
             f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells, blank, out, check,
-            stream, loss, wgrad_f32))
+            None, loss, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss, wgrad_f32=wgrad_f32)
     if out is None:
         out = Outputs(f, g, W_f, W_g, W_o, b_o, dims)
-    if stream is None:
-        stream = torch.cuda.current_stream(f.device)
     rc = lib().frnnt_fwd_bwd(ctypes.byref(dims), _ptr(f), _ptr(g), _ptr(W_f), _ptr(W_g), _ptr(W_o), _ptr(b_o),
                              _ptr(labels), _ptr(T_len), _ptr(U_len), _ptr(grad_loss), _ptr(out.loss),
                              _ptr(out.df), _ptr(out.dg), _ptr(out.dW_f), _ptr(out.dW_g), _ptr(out.dW_o),
                              _ptr(out.db_o), _ptr(out.workspace), out.workspace.numel(), _ptr(out.status),
-                             ctypes.c_void_p(stream.cuda_stream))
+                             _queue(f.device))
     if rc != OK:
         raise FrnntError(rc, error_string(rc))
     if check:
@@ -376,21 +391,24 @@ def fwd_bwd_noalloc(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss=No
     FrnntError(FRNNT_ERR_WORKSPACE) when these dims need more than
     NOALLOC_MAX_BYTES of scratch."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out)
+    there = _loss_place(f.device, stream)
+    if there is not None:
+        with there:
+            return fwd_bwd_noalloc(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells,
+                                   blank, out, check, None, loss, dropout)
     if dropout is not None:
-        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_noalloc(
+        return _with_dropout(dropout, f, g, out, lambda f, g: fwd_bwd_noalloc(
             f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, mode, path, chunk_cells, blank, out, check,
-            stream, loss))
+            None, loss))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss)
     if out is None:
         out = Outputs(f, g, W_f, W_g, W_o, b_o, dims, with_workspace=False)
-    if stream is None:
-        stream = torch.cuda.current_stream(f.device)
     rc = lib().frnnt_fwd_bwd_noalloc(ctypes.byref(dims), _ptr(f), _ptr(g), _ptr(W_f), _ptr(W_g), _ptr(W_o),
                                      _ptr(b_o), _ptr(labels), _ptr(T_len), _ptr(U_len), _ptr(grad_loss),
                                      _ptr(out.loss), _ptr(out.df), _ptr(out.dg), _ptr(out.dW_f), _ptr(out.dW_g),
                                      _ptr(out.dW_o), _ptr(out.db_o), _ptr(out.status),
-                                     ctypes.c_void_p(stream.cuda_stream))
+                                     _queue(f.device))
     if rc != OK:
         msg = error_string(rc)
         if rc == 3:
@@ -447,21 +465,24 @@ def fwd_bwd_pruned(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S: in
     keeps, for frame t of utterance b, the S label positions
     bounds[b,t] <= u < bounds[b,t] + S (bounds: int32 [B, T] on the device)."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, bounds=bounds, wgrad_f32=wgrad_f32)
+    there = _loss_place(f.device, stream)
+    if there is not None:
+        with there:
+            return fwd_bwd_pruned(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S, grad_loss, mode, path,
+                                  chunk_cells, blank, out, check, None, loss, wgrad_f32, dropout)
     if dropout is not None:
-        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_pruned(
+        return _with_dropout(dropout, f, g, out, lambda f, g: fwd_bwd_pruned(
             f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, bounds, S, grad_loss, mode, path, chunk_cells, blank, out,
-            check, stream, loss, wgrad_f32))
+            check, None, loss, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, path, chunk_cells, blank, loss, S, wgrad_f32=wgrad_f32)
     if out is None:
         out = Outputs(f, g, W_f, W_g, W_o, b_o, dims)
-    if stream is None:
-        stream = torch.cuda.current_stream(f.device)
     rc = lib().frnnt_fwd_bwd_pruned(ctypes.byref(dims), _ptr(f), _ptr(g), _ptr(W_f), _ptr(W_g), _ptr(W_o),
                                     _ptr(b_o), _ptr(labels), _ptr(T_len), _ptr(U_len), _ptr(bounds),
                                     _ptr(grad_loss), _ptr(out.loss), _ptr(out.df), _ptr(out.dg), _ptr(out.dW_f),
                                     _ptr(out.dW_g), _ptr(out.dW_o), _ptr(out.db_o), _ptr(out.workspace),
-                                    out.workspace.numel(), _ptr(out.status), ctypes.c_void_p(stream.cuda_stream))
+                                    out.workspace.numel(), _ptr(out.status), _queue(f.device))
     if rc != OK:
         raise FrnntError(rc, error_string(rc))
     if check:
@@ -482,23 +503,26 @@ def fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durati
     and db_d)."""
     _check_call(f, g, W_f, W_g, W_o, b_o, labels, T_len, U_len, grad_loss, out, W_d=W_d, b_d=b_d,
                 wgrad_f32=wgrad_f32)
+    there = _loss_place(f.device, stream)
+    if there is not None:
+        with there:
+            return fwd_bwd_tdt(f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durations, grad_loss, mode,
+                               chunk_cells, blank, out, check, None, wgrad_f32, dropout)
     if dropout is not None:
-        return _with_dropout(dropout, f, g, out, stream, lambda f, g: fwd_bwd_tdt(
+        return _with_dropout(dropout, f, g, out, lambda f, g: fwd_bwd_tdt(
             f, g, W_f, W_g, W_o, b_o, W_d, b_d, labels, T_len, U_len, durations, grad_loss, mode, chunk_cells, blank,
-            out, check, stream, wgrad_f32))
+            out, check, None, wgrad_f32))
     dtype = "bf16" if f.dtype == torch.bfloat16 else "f32"
     dims = dims_of(f, g, W_o, dtype, mode, "auto", chunk_cells, blank, "marginal", 0, tuple(durations),
                    wgrad_f32=wgrad_f32)
     if out is None:
         out = Outputs(f, g, W_f, W_g, W_o, b_o, dims, W_d=W_d, b_d=b_d)
-    if stream is None:
-        stream = torch.cuda.current_stream(f.device)
     rc = lib().frnnt_fwd_bwd_tdt(ctypes.byref(dims), _ptr(f), _ptr(g), _ptr(W_f), _ptr(W_g), _ptr(W_o), _ptr(b_o),
                                  _ptr(W_d), _ptr(b_d), _ptr(labels), _ptr(T_len), _ptr(U_len), _ptr(grad_loss),
                                  _ptr(out.loss), _ptr(out.df), _ptr(out.dg), _ptr(out.dW_f), _ptr(out.dW_g),
                                  _ptr(out.dW_o), _ptr(out.db_o), _ptr(out.dW_d), _ptr(out.db_d),
                                  _ptr(out.workspace), out.workspace.numel(), _ptr(out.status),
-                                 ctypes.c_void_p(stream.cuda_stream))
+                                 _queue(f.device))
     if rc != OK:
         raise FrnntError(rc, error_string(rc))
     if check:
