@@ -63,6 +63,12 @@ FRNNT_API int frnnt_test_lose_gemm_loads(int n);
  * between calls).  Returns the launches that were still to come. */
 FRNNT_API int frnnt_test_lose_scan_maps(int n, int round, int quit, int tries);
 
+/* Test setting of the recurrence: while on, every request that it makes of the
+ * runtime for clusters of blocks fails (it asks for more shared memory than a
+ * device has), so that a sequence gets one block.  Process-wide, not
+ * thread-safe (set it between calls).  Returns the previous setting. */
+FRNNT_API int frnnt_test_refuse_clusters(int on);
+
 /* The K-slice count the tensor-core GEMM takes for a split-K launch (host
  * only, no GPU needed): mn output tiles on `workers` persistent CTAs (or CTA
  * pairs), kblocks K blocks of 64.  It minimises rounds x (K blocks per unit +

@@ -271,6 +271,8 @@ int gemm_tc(const GemmTcArgs& g, cudaStream_t st);
 int lose_gemm_loads(int n);
 // Test setting (frnnt_test_lose_scan_maps).
 int lose_scan_maps(int n, int round, bool quit, int tries);
+// Test setting (frnnt_test_refuse_clusters).
+bool refuse_clusters(bool on);
 // K slices of a split-K GEMM (frnnt_gemm_tc.cu): mn output tiles on `workers`
 // persistent CTAs or CTA pairs, kblocks 64-wide K blocks.
 int auto_splits(int mn, int workers, int kblocks);

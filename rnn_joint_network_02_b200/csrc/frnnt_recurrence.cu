@@ -647,19 +647,25 @@ constexpr int kSlack = 16;
 template <typename T, int ARRAYS>
 constexpr int kMostBytes = (int)sizeof(Stage<T>) * ARRAYS * stages_of(ARRAYS) + kSlack;
 
+// Test setting (frnnt_test_refuse_clusters): the runtime is asked for more shared memory than there is.
+bool g_refuse_clusters = false;
+
 // How many clusters of CL blocks run at a time on the current device (any number
-// with CL = 1), and the kernel made ready for that much shared memory; -1: failed.
+// with CL = 1), and the kernel made ready for that much shared memory.  Clusters
+// that the runtime refuses do not run: 0, and its error is taken back, since the
+// call goes on with other sizes; a single block that it refuses: -1, an error.
 template <typename T, int ARRAYS, int CL, auto kernel>
 int resident() {
   static std::atomic<int> known[kDeviceSlots];   // (+ 1)
   std::atomic<int>& here = known[current_device()];
-  if (const int n = here.load(std::memory_order_acquire)) return n - 1;
+  const bool refuse = CL > 1 && g_refuse_clusters;
+  if (const int n = here.load(std::memory_order_acquire); n && !refuse) return n - 1;
   constexpr int bytes = kMostBytes<T, ARRAYS>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return -1;
-  if (CL > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return -1;
+  bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, refuse ? INT_MAX : bytes) ==
+            cudaSuccess;
+  if (CL > 8) ok = ok && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
   int n = INT_MAX - 1;
-  if (CL > 1) {
+  if (CL > 1 && ok) {
     cudaLaunchAttribute size;
     size.id = cudaLaunchAttributeClusterDimension;
     size.val.clusterDim.x = CL;
@@ -670,9 +676,14 @@ int resident() {
     config.dynamicSmemBytes = bytes;
     config.attrs = &size;
     config.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &config) != cudaSuccess || n < 0) return -1;
+    ok = cudaOccupancyMaxActiveClusters(&n, kernel, &config) == cudaSuccess && n >= 0;
   }
-  here.store(n + 1, std::memory_order_release);
+  if (!ok) {
+    if (CL == 1) return -1;
+    cudaGetLastError();
+    n = 0;
+  }
+  if (!refuse) here.store(n + 1, std::memory_order_release);
   return n;
 }
 
@@ -792,6 +803,12 @@ int bwd_of(bool vec, const frnnt_recurrence_dims& d, const void* x, const void* 
 }
 
 }  // namespace
+
+bool refuse_clusters(bool on) {
+  const bool prev = g_refuse_clusters;
+  g_refuse_clusters = on;
+  return prev;
+}
 
 int lose_scan_maps(int n, int round, bool quit, int tries) {
   const int prev = g_trials;

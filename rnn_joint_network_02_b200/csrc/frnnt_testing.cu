@@ -37,6 +37,8 @@ extern "C" FRNNT_API int frnnt_test_lose_scan_maps(int n, int round, int quit, i
   return frnnt::lose_scan_maps(n, round, quit != 0, tries);
 }
 
+extern "C" FRNNT_API int frnnt_test_refuse_clusters(int on) { return frnnt::refuse_clusters(on != 0); }
+
 extern "C" FRNNT_API int frnnt_test_auto_splits(int mn, int workers, int kblocks) {
   return frnnt::auto_splits(mn, workers, kblocks);
 }

@@ -32,7 +32,7 @@ MAX_DURATIONS = 8
 MAX_TOKENS, MAX_TOP, NO_TOKEN, SCAN_CHUNK = 32, 32, -1, 128
 NOALLOC_MAX_BYTES = 64 * 1024 * 1024
 TEST_HOOKS = ("frnnt_test_gemm_bf16", "frnnt_test_joint_variant", "frnnt_test_lose_gemm_loads",
-              "frnnt_test_lose_scan_maps")
+              "frnnt_test_lose_scan_maps", "frnnt_test_refuse_clusters")
 
 
 class Dims(ctypes.Structure):
@@ -138,6 +138,8 @@ def lib() -> ctypes.CDLL:
         L.frnnt_test_lose_gemm_loads.restype = ctypes.c_int
         L.frnnt_test_lose_scan_maps.argtypes = [ctypes.c_int] * 4
         L.frnnt_test_lose_scan_maps.restype = ctypes.c_int
+        L.frnnt_test_refuse_clusters.argtypes = [ctypes.c_int]
+        L.frnnt_test_refuse_clusters.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -450,6 +452,12 @@ def lose_scan_maps(n: int, round: int = 0, quit: bool = False, tries: int = 200)
     (or gives up after it), so bounded waits run out and the status word gets
     STATUS_TIMEOUT.  Returns the launches that were still to come."""
     return int(lib().frnnt_test_lose_scan_maps(int(n), int(round), int(quit), int(tries)))
+
+
+def refuse_clusters(on: bool) -> bool:
+    """Test setting (include/frnnt_testing.h): the recurrence's requests for
+    clusters of blocks fail while it is on.  Returns the previous setting."""
+    return bool(lib().frnnt_test_refuse_clusters(int(on)))
 
 
 def set_joint_variant(variant: int) -> int:

@@ -10,7 +10,9 @@ import time
 import pytest
 import torch
 
+from oracle import ops_oracle as O
 from rnn_joint_network_02_b200 import frnnt
+from tests.test_logprob_gpu import close, host, ints
 from tests.test_recurrence_gpu import make
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +78,31 @@ def test_the_limit_itself(cuda_ok, lose_maps):
     took = _times_out(lambda: frnnt.recurrence(x, gate))
     assert took < 15, took
     assert torch.equal(frnnt.recurrence(x, gate).h, want)
+
+
+@pytest.mark.parametrize("B,T,D,layout,dtype", [(1, 4200, 64, "plain", "bf16"), (3, 700, 65, "offset", "f32")])
+def test_refused_clusters_are_no_error(cuda_ok, B, T, D, layout, dtype):
+    """Clusters that the runtime refuses are done without: the call succeeds, its results are those of one block a
+    sequence, and no error is left for the next call."""
+    x, gate, lengths, h0, dh, dl = make(B, T, D, dtype, layout, seed=53)
+    run = lambda: frnnt.recurrence(x, gate, lengths=lengths, h0=h0)  # noqa: E731
+    back = lambda r: frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)  # noqa: E731
+    assert not frnnt.refuse_clusters(True)
+    try:
+        r = run()
+        d = back(r)
+        assert frnnt.lose_scan_maps(1) == 0
+        again = run()
+        assert frnnt.lose_scan_maps(0) == 1, "no launch had clusters"
+    finally:
+        frnnt.refuse_clusters(False)
+    assert torch.equal(r.h, again.h)
+    torch.ones(1, device="cuda").add_(1).item()      # (would report an error that was left)
+    ref = O.recurrence(host(x), host(gate), ints(lengths), host(h0), dtype)
+    want = O.recurrence_bwd(host(x), host(gate), ref, host(dh), ints(lengths), host(dl), dtype)
+    close(r.h, ref["h"], ref["h_tol"], "h")
+    for k in KEYS:
+        close(d[k], want[k], want[k + "_tol"], k)
+    frnnt.lose_scan_maps(1)
+    with pytest.raises(frnnt.FrnntStatusError):     # granted again
+        run()
