@@ -26,14 +26,40 @@ HALF_STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
 
 
 # ------------------------------------------------------------------ token log-probabilities
+def _row_tolerances(row, m, ls, V):
+    """Of a row's lse, entropy, and log-probabilities (an array, one a column).
+    Magnitudes count where they carry probability: a value that masks a column
+    (-inf, or the type's lowest) enters no sum, and a shift of all logits enters
+    none either, since their differences from the maximum are formed first."""
+    if not np.isfinite(m):    # an empty row's values are exact, one with NaN or +inf has none
+        return 0.0, 0.0, np.zeros_like(row)
+    d, p = np.where(row > -np.inf, m - row, 0.0), np.exp((row - m) - ls)
+    # A term of the sum, exp(-d): the difference, its product with log2 e and that constant are rounded, 3 * 2^-24 d in
+    # the exponent; the function itself, and the orders of summing, are UNIT each.  The sum's relative error is the
+    # terms' mean error (at 1000 and more, where p is 0, d is cut off so that 0 times it is 0).
+    near = np.minimum(d, 1000.0)
+    term = 4 * UNIT + 2.0 ** -22 * near
+    total = (p * term).sum()
+    # its logarithm, and the sum of the maximum and that, rounded once each
+    lse_tol = total + 2.0 ** -23 * np.log(V) + 2.0 ** -24 * abs(m + ls) + 2.0 ** -126
+    # difference from the maximum, logarithm, and their difference; of columns of any probability
+    log_p = total + 2.0 ** -23 * (d + np.log(V) + 1.0)
+    # H = log(sum) + sum p d: the terms' errors against d, d's own, the quotient by the sum, and roundings
+    mean = (p * near).sum()
+    entropy_tol = total * (1 + mean) + (p * near * (term + 2.0 ** -22)).sum() + 2.0 ** -22 * (np.log(V) + mean + 1)
+    return lse_tol, entropy_tol, log_p
+
+
 def token_logprobs(z, tokens=None, top=0):
     """z [N, V] float64 (-inf allowed), tokens [N, K] ints.  Returns a dict: logp
     [N, K], entropy [N], lse [N], top_logp, top_ids [N, top] and logp_tol,
-    entropy_tol, lse_tol, top_tol."""
+    entropy_tol, lse_tol, top_tol; and lse in two parts, max and log_sum [N],
+    since their sum loses the second one where the logits are huge (even in 64
+    bits: rows of the type's lowest value)."""
     N, V = z.shape
     K = 0 if tokens is None else tokens.shape[1]
     out = dict(logp=np.zeros((N, K)), entropy=np.zeros(N), lse=np.zeros(N), top_logp=np.zeros((N, top)),
-               top_ids=np.zeros((N, top), dtype=np.int64))
+               top_ids=np.zeros((N, top), dtype=np.int64), max=np.zeros(N), log_sum=np.zeros(N))
     tol = dict(logp_tol=np.zeros((N, K)), entropy_tol=np.zeros(N), lse_tol=np.zeros(N), top_tol=np.zeros((N, top)))
     for n in range(N):
         row = z[n]
@@ -42,27 +68,24 @@ def token_logprobs(z, tokens=None, top=0):
         ids = order[:top]
         given = [] if K == 0 else [int(t) for t in tokens[n]]
         if np.isnan(row).any() or np.isposinf(row).any():
-            lse = entropy = np.nan
+            m, ls, entropy = np.nan, 0.0, np.nan
         elif np.isneginf(row).all():
-            lse, entropy = -np.inf, 0.0
+            m, ls, entropy = -np.inf, 0.0, 0.0
         else:
             m = row.max()
-            lse = m + np.log(np.exp(row - m).sum())
-            lp = row[row > -np.inf] - lse
+            ls = np.log(np.exp(row - m).sum())
+            lp = (row[row > -np.inf] - m) - ls
             entropy = -(np.exp(lp) * lp).sum()
-        one = (lambda t: -np.inf if np.isneginf(lse) else row[t] - lse)
-        out["lse"][n], out["entropy"][n] = lse, entropy
+        lse = m + ls
+        one = (lambda t: -np.inf if np.isneginf(m) else (row[t] - m) - ls)
+        out["lse"][n], out["entropy"][n], out["max"][n], out["log_sum"][n] = lse, entropy, m, ls
         out["top_ids"][n] = ids
         out["top_logp"][n] = [one(j) for j in ids]
         out["logp"][n] = [0.0 if t == NO_TOKEN else one(t) for t in given]
-        # the log of the sum is off by the sum's relative error; a value in fp32 by half a step of its size, and so
-        # are the logit's difference from the maximum and the log-sum-exp that it is taken from
-        big = np.nanmax(np.abs(np.where(np.isfinite(row), row, 0.0)))
-        tol["lse_tol"][n] = 4 * UNIT + 2.0 ** -23 * (big + np.log(V) + 1)
-        tol["logp_tol"][n] = 4 * UNIT + 2.0 ** -23 * (big + np.log(V) + 1)
-        tol["top_tol"][n] = tol["lse_tol"][n]
-        # sum p (log p): each term p |log p| with the relative error of p, which is that of its exponent's size
-        tol["entropy_tol"][n] = (4 * UNIT + 2.0 ** -23 * (big + 1)) * (np.log(V) + 2)
+        with np.errstate(invalid="ignore", over="ignore", under="ignore"):
+            tol["lse_tol"][n], tol["entropy_tol"][n], near = _row_tolerances(row, m, ls, V)
+            tol["logp_tol"][n] = [0.0 if t == NO_TOKEN else near[t] for t in given]
+            tol["top_tol"][n] = [near[j] for j in ids]
     out.update(tol)
     return out
 
@@ -77,11 +100,12 @@ def token_logprobs_bwd(z, tokens, fwd, dlogp=None, dentropy=None, dtop=None, dty
         if np.isneginf(lse):
             continue
         with np.errstate(invalid="ignore"):
-            lp = z[n] - lse
+            lp = (z[n] - fwd["max"][n]) - fwd["log_sum"][n]
             p = np.exp(lp)
         safe = np.where(p > 0, lp, 0.0) if not np.isnan(lse) else lp
-        big = np.nanmax(np.abs(np.where(np.isfinite(z[n]), z[n], 0.0)))
-        rel = 4 * UNIT + 2.0 ** -22 * (big + np.log(V) + 1)       # of p: its exponent's absolute error
+        # of p, which is taken from lse rounded to fp32: its exponent's absolute error, where p is not 0
+        with np.errstate(invalid="ignore", over="ignore"):
+            rel = 4 * UNIT + fwd["lse_tol"][n] + 2.0 ** -22 * np.where(p > 0, np.abs(lp), 0.0)
         coef = []
         if dlogp is not None:
             coef += [(int(tokens[n, k]), dlogp[n, k]) for k in range(dlogp.shape[1]) if int(tokens[n, k]) != NO_TOKEN]
@@ -97,7 +121,9 @@ def token_logprobs_bwd(z, tokens, fwd, dlogp=None, dentropy=None, dtop=None, dty
             H, d = fwd["entropy"][n], dentropy[n]
             dz[n] -= d * p * (safe + H)
             tol[n] += abs(d) * p * (2 * rel * (np.abs(safe) + abs(H) + 1) + fwd["entropy_tol"][n])
-        tol[n] += HALF_STEP[dtype] * (np.abs(dz[n]) + tol[n]) + 2.0 ** -126
+        # a p below 2^-126 may count as 0
+        gone = 2.0 ** -126 * (1 + size + (0.0 if dentropy is None else 200 * abs(dentropy[n])))
+        tol[n] += HALF_STEP[dtype] * (np.abs(dz[n]) + tol[n]) + gone
     return dz, tol
 
 
