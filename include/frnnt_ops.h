@@ -48,12 +48,14 @@ typedef struct {
   frnnt_dtype dtype;   /* element type of logits and dlogits                                   */
   long long ld;        /* elements from one row of logits to the next, >= V                    */
   long long ldd;       /* the same for dlogits (backward only), >= V                           */
+  float* lse_rest;     /* [N] fp32 on the device or NULL: written by the forward call, read by
+                          the backward call (see there)                                        */
 } frnnt_logprob_dims;
 
 /* For every row z of logits [N, V], with lse = log sum_j exp(z_j) and log p_j = z_j - lse:
  *   logp     [N, K] fp32    log p_{tokens[n,k]}; 0 where tokens[n,k] is FRNNT_NO_TOKEN
  *   entropy  [N] fp32       -sum_j p_j log p_j  (natural logarithm; p log p = 0 at p = 0)
- *   lse      [N] fp32
+ *   lse      [N] fp32; lse_rest [N], where given, is what rounding to fp32 took from it
  *   top_logp [N, top] fp32, top_ids [N, top] int32   the `top` largest logits' log-probabilities, largest
  *                           first, and their columns; equal logits: the lowest column first
  * tokens [N, K] int32 (may be NULL with K = 0); the same token may be given more than once.  logp / top_logp /
@@ -72,7 +74,9 @@ FRNNT_API int frnnt_token_logprobs(const frnnt_logprob_dims* d, const void* logi
  * lse, entropy and top_ids are the forward call's; dlogp [N, K], dentropy [N] and dtop [N, top] are fp32 and may
  * each be NULL (no such term; tokens and top_ids are then not read, entropy only with dentropy).  A token that is
  * FRNNT_NO_TOKEN contributes nothing; a token or top id outside [0, V) otherwise sets FRNNT_STATUS_LABEL and
- * contributes nothing.  dlogits [N, ldd] has the type of the logits, rounded once; it may be the logits' own
+ * contributes nothing.  p_j comes from lse and, where given, lse_rest, as the forward call wrote them; without
+ * lse_rest every p_j is off by a factor of exp(2^-24 |lse|) at most, and in a row of huge logits (all of them the
+ * type's lowest value, say) p means nothing.  dlogits [N, ldd] has the type of the logits, rounded once; it may be the logits' own
  * memory (same address and ldd = ld).  A row of -inf only gets zeros, and so does a row without any term (no
  * given token, dtop and dentropy NULL) whatever it holds; elements of the rows past V are not written. */
 FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, const void* logits, const int32_t* tokens,

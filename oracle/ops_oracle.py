@@ -103,9 +103,12 @@ def token_logprobs_bwd(z, tokens, fwd, dlogp=None, dentropy=None, dtop=None, dty
             lp = (z[n] - fwd["max"][n]) - fwd["log_sum"][n]
             p = np.exp(lp)
         safe = np.where(p > 0, lp, 0.0) if not np.isnan(lse) else lp
-        # of p, which is taken from lse rounded to fp32: its exponent's absolute error, where p is not 0
+        # of p, where it is not 0: its exponent's absolute error.  The sum's logarithm has the sum's relative error
+        # (that of the log-probability of the maximum, with its roundings); z - lse is rounded at its own size, which
+        # is within log(sum) <= ln V of log p's; and two products at theirs
         with np.errstate(invalid="ignore", over="ignore"):
-            rel = 4 * UNIT + fwd["lse_tol"][n] + 2.0 ** -22 * np.where(p > 0, np.abs(lp), 0.0)
+            of_sum = _row_tolerances(z[n], fwd["max"][n], fwd["log_sum"][n], V)[2].min()
+            rel = 4 * UNIT + of_sum + 2.0 ** -22 * (np.where(p > 0, np.abs(lp), 0.0) + np.log(V) + 1)
         coef = []
         if dlogp is not None:
             coef += [(int(tokens[n, k]), dlogp[n, k]) for k in range(dlogp.shape[1]) if int(tokens[n, k]) != NO_TOKEN]

@@ -646,4 +646,4 @@ extern "C" const char* frnnt_error_string(int code) {
   return "unknown frnnt code";
 }
 
-extern "C" const char* frnnt_version(void) { return "0.1.0"; }
+extern "C" const char* frnnt_version(void) { return "0.2.0"; }

@@ -189,6 +189,7 @@ struct FwdParams {
   const int32_t* tokens;
   float *logp, *entropy, *lse, *top_logp;
   int32_t *top_ids, *status;
+  float* lse_rest;   // lse where it is not wanted
 };
 
 // What a lane holds of a row: kVecs vectors, from vector `base` on, 32 apart.
@@ -372,10 +373,14 @@ __device__ __noinline__ uint64_t best_in_order(const T* p, int V, int top, uint6
 }
 
 // A row's values from its joined statistics; ls = ln st.s.  st.s is 0 where
-// nothing but -inf was seen.
+// nothing but -inf was seen.  The sum of m and ls goes out with what rounding
+// took from it (the two-sum of Knuth), which is all of ls where m is huge.
 __device__ __forceinline__ void write_stats(const FwdParams& p, long long n, const Stats& st, float ls) {
   const bool empty = st.s == 0.f;
-  p.lse[n] = empty ? -INFINITY : st.m + ls;
+  const float lse = st.m + ls, part = lse - st.m;
+  const float rest = (st.m - (lse - part)) + (ls - part);
+  p.lse_rest[n] = empty ? 0.f : rest;   // (first: its place may be lse's)
+  p.lse[n] = empty ? -INFINITY : lse;
   p.entropy[n] = empty ? 0.f : fmaf(st.w / st.s, -kLn2, ls);
 }
 __device__ __forceinline__ void write_token(const FwdParams& p, long long n, int k, const Stats& st, float ls,
@@ -765,6 +770,7 @@ struct BwdParams {
   const int32_t *tokens, *top_ids;
   const float *lse, *entropy, *dlogp, *dentropy, *dtop;
   int32_t* status;
+  const float* lse_rest;   // or NULL: 0
 };
 
 template <typename T>
@@ -786,9 +792,16 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)]
 
 // The gradient of a row: dz_j = p_j (A + B log2 p_j) with -A = sum of the
 // coefficients + dentropy entropy and -B = dentropy ln2, plus the coefficients
-// of column j.
+// of column j.  With d_j = (z_j - l) log2 e, l the log-sum-exp rounded to fp32, and c
+// what rounding took from it, log2 p_j = d_j + c: without c an offset of all
+// logits, |l| 2^-24, would be an error of every p (and p = 1 in a row of the type's
+// lowest value).  dz_j = 2^d_j 2^c (A + B c + B d_j) costs nothing an element.
 struct Slope {
-  float l, A, B;   // l: log-sum-exp
+  float l, A, B;
+  static __device__ __forceinline__ Slope of(float l, float rest, float A, float B) {
+    const float c = -kLog2e * rest, f = exp2_approx(c);
+    return Slope{l, f * fmaf(B, c, A), f * B};
+  }
   __device__ __forceinline__ float at(float z) const {
     const float d = at_least((z - l) * kLog2e, kFloor);
     return exp2_approx(d) * fmaf(B, d, A);
@@ -822,6 +835,9 @@ struct Slope {
     }
   }
 };
+__device__ __forceinline__ float rest_of(const BwdParams& p, long long n) {
+  return p.lse_rest ? p.lse_rest[n] : 0.f;
+}
 // A lane's vectors, 32 apart, of a warp's share [base, end) of a row.  SKEW: rows
 // may start elsewhere in their 16 bytes than the gradient's.  Then vector v of 16-
 // bit elements lies in two aligned ones, v and v + 1 (both hold some of the row);
@@ -933,7 +949,7 @@ __global__ void __launch_bounds__(kWarps * 32, SKEW && sizeof(T) == 2 ? 2 : 3)
       }
       sum += coef[k];
     }
-    if (any) own = Slope{p.lse[mine], -fmaf(de, h, sum), -de * kLn2};
+    if (any) own = Slope::of(p.lse[mine], rest_of(p, mine), -fmaf(de, h, sum), -de * kLn2);
   }
   for (int i = 0; i < count; ++i) {
     const Slope g{__shfl_sync(kAll, own.l, i), __shfl_sync(kAll, own.A, i), __shfl_sync(kAll, own.B, i)};
@@ -994,6 +1010,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdPara
 #pragma unroll
   for (int e = 0; e < C; ++e) z[e] = g + G * e < p.V ? to_f32<T>(row[g + G * e]) : 0.f;
   const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
+  const float rest = rest_of(p, n);
   bool any = p.dentropy != nullptr;
   const int nk = p.dlogp ? p.K : 0, slots = nk + (p.dtop ? p.top : 0);
 #pragma unroll 2
@@ -1009,7 +1026,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdPara
       atomicOr(p.status, FRNNT_STATUS_LABEL);
     }
   }
-  const Slope s{l, -fmaf(de, h, sum), -de * kLn2};
+  const Slope s = Slope::of(l, rest, -fmaf(de, h, sum), -de * kLn2);
 #pragma unroll
   for (int e = 0; e < C; ++e)   // a row without any term, or with nothing left by its mask, gets zeros
     if (g + G * e < p.V) out[g + G * e] = from_f32<T>(!any || l == -INFINITY ? 0.f : s.at(z[e]) + total[e]);
@@ -1053,6 +1070,7 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
     }
   }
   const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
+  const float rest = rest_of(p, n);
   float sum = coef[0] + coef[1];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
@@ -1065,7 +1083,7 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   }
   // a row without any term, or with nothing left by its mask, gets zeros
   const bool none = l == -INFINITY || (!p.dentropy && !__any_sync(kAll, id[0] >= 0 || id[1] >= 0));
-  const Slope g{l, -fmaf(de, h, sum), -de * kLn2};
+  const Slope g = Slope::of(l, rest, -fmaf(de, h, sum), -de * kLn2);
   auto patch = [&](int lo, int hi) {   // columns lo .. hi - 1 have been written by this warp
     __syncwarp();
 #pragma unroll
@@ -1236,13 +1254,14 @@ extern "C" FRNNT_API int frnnt_token_logprobs(const frnnt_logprob_dims* d, const
     return FRNNT_ERR_NULL;
   if ((uintptr_t)logits % (d->dtype == FRNNT_BF16 ? 2 : 4)) return FRNNT_ERR_ALIGN;
   for (const void* p : {(const void*)tokens, (const void*)logp, (const void*)entropy, (const void*)lse,
-                        (const void*)top_logp, (const void*)top_ids, (const void*)status})
+                        (const void*)top_logp, (const void*)top_ids, (const void*)status, (const void*)d->lse_rest})
     if ((uintptr_t)p % 4) return FRNNT_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs", st);
-    const FwdParams p{d->N, d->V, d->K, d->top, d->ld, tokens, logp, entropy, lse, top_logp, top_ids, status};
+    const FwdParams p{d->N, d->V, d->K, d->top, d->ld, tokens, logp, entropy, lse, top_logp, top_ids, status,
+                      d->lse_rest ? d->lse_rest : lse};
     if (d->dtype == FRNNT_BF16) {
       auto* z = (const __nv_bfloat16*)logits;
       d->top ? launch_fwd<__nv_bfloat16, true>(p, z, st) : launch_fwd<__nv_bfloat16, false>(p, z, st);
@@ -1268,14 +1287,14 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   const size_t es = d->dtype == FRNNT_BF16 ? 2 : 4;
   if ((uintptr_t)logits % es || (uintptr_t)dlogits % es) return FRNNT_ERR_ALIGN;
   for (const void* p : {(const void*)tokens, (const void*)lse, (const void*)entropy, (const void*)top_ids,
-                        (const void*)dlogp, (const void*)dentropy, (const void*)dtop, (const void*)status})
+                        (const void*)dlogp, (const void*)dentropy, (const void*)dtop, (const void*)status, (const void*)d->lse_rest})
     if ((uintptr_t)p % 4) return FRNNT_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
   cudaGetLastError();   // clear a stale error so it is not reported as ours
   {
     StageScope sc("token_logprobs_bwd", st);
     const BwdParams p{d->N, d->V, d->K,    d->top, 1,     0,        d->ld, d->ldd,
-                      tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,  status};
+                      tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,  status, d->lse_rest};
     if (d->dtype == FRNNT_BF16) launch_bwd(p, (const __nv_bfloat16*)logits, (__nv_bfloat16*)dlogits, st);
     else launch_bwd(p, (const float*)logits, (float*)dlogits, st);
   }

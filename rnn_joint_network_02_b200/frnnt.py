@@ -45,7 +45,8 @@ class Dims(ctypes.Structure):
 
 class LogprobDims(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int), ("V", ctypes.c_int), ("K", ctypes.c_int), ("top", ctypes.c_int),
-                ("dtype", ctypes.c_int), ("ld", ctypes.c_longlong), ("ldd", ctypes.c_longlong)]
+                ("dtype", ctypes.c_int), ("ld", ctypes.c_longlong), ("ldd", ctypes.c_longlong),
+                ("lse_rest", ctypes.c_void_p)]
 
 
 class RecurrenceDims(ctypes.Structure):
@@ -632,14 +633,15 @@ def _at(t):
 class LogProbs:
     """Outputs of token_logprobs: logp [N, K], entropy [N], lse [N], top_logp
     [N, top] (fp32) and top_ids [N, top] (int32); logp is None without tokens,
-    the last two are None with top = 0."""
-    __slots__ = ("logp", "entropy", "lse", "top_logp", "top_ids")
+    the last two are None with top = 0.  lse_rest [N] is what rounding took from
+    lse, for the backward call."""
+    __slots__ = ("logp", "entropy", "lse", "lse_rest", "top_logp", "top_ids")
 
     def __init__(self, N, K, top, device):
         def new(dtype, *shape):
             return torch.empty(shape, dtype=dtype, device=device)
         self.logp = new(_F32T, N, K) if K else None
-        self.entropy, self.lse = new(_F32T, N), new(_F32T, N)
+        self.entropy, self.lse, self.lse_rest = (new(_F32T, N) for _ in range(3))
         self.top_logp = new(_F32T, N, top) if top else None
         self.top_ids = new(_I32, N, top) if top else None
 
@@ -650,6 +652,7 @@ class LogProbs:
         r.logp = _new((N, K), (K, 1), _F32T) if K else None
         r.entropy = _new((N,), (1,), _F32T)
         r.lse = _new((N,), (1,), _F32T)
+        r.lse_rest = _new((N,), (1,), _F32T)
         if top:
             r.top_logp = _new((N, top), (top, 1), _F32T)
             r.top_ids = _new((N, top), (top, 1), _I32)
@@ -659,19 +662,27 @@ class LogProbs:
 
 
 def _check_logprobs(logits, tokens, top):
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [N, V]")
-    dt = _float_type("logits", logits)
-    N, V = logits.shape
+    dt = _TYPES.get(logits.dtype)
+    if dt is None:
+        _float_type("logits", logits)
+    N, V = shape
     K = 0
     if tokens is not None:
-        if tokens.dim() != 2:
+        shape = tokens.shape
+        if len(shape) != 2:
             raise ValueError("tokens must be [N, K]")
-        K = tokens.shape[1]
-        _expect("tokens", tokens, (N, K), _I32, logits.device)
-    if not 0 <= top <= min(V, MAX_TOP) or K > MAX_TOKENS:
+        K = shape[1]
+        if shape[0] != N or tokens.dtype is not _I32 or tokens.device != logits.device or not tokens.is_contiguous():
+            _expect("tokens", tokens, (N, K), _I32, logits.device)
+    if top < 0 or top > V or top > MAX_TOP or K > MAX_TOKENS:
         raise ValueError(f"at most {MAX_TOKENS} tokens and min(V, {MAX_TOP}) alternatives per row")
-    return dt, N, V, K
+    sn, sc = logits.stride()
+    if sc != 1 and V > 1:
+        raise ValueError("the columns of logits must be adjacent (stride 1)")
+    return dt, N, V, K, sn if N > 1 else max(V, sn)
 
 
 def _check_result(fwd, N, K, top, dev):
@@ -684,6 +695,7 @@ def _check_result(fwd, N, K, top, dev):
             raise ValueError(f"the result has no {name}")
     _expect("entropy", fwd.entropy, (N,), f32, dev)
     _expect("lse", fwd.lse, (N,), f32, dev)
+    _expect("lse_rest", fwd.lse_rest, (N,), f32, dev)
 
 
 def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, check=True, stream=None) -> LogProbs:
@@ -694,8 +706,7 @@ def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, chec
     -inf logits have probability 0.  ``out``: an earlier call's result, written
     again.  With ``check`` the device status is read back (which synchronises)
     and tokens outside [0, V) raise FrnntStatusError."""
-    dt, N, V, K = _check_logprobs(logits, tokens, top)
-    ld = _rows("logits", logits)
+    dt, N, V, K, ld = _check_logprobs(logits, tokens, top)
     dev = logits.device
     if out is not None:
         _check_result(out, N, K, top, dev)
@@ -706,10 +717,11 @@ def token_logprobs(logits, tokens=None, top=0, out: LogProbs | None = None, chec
     if out is None:
         out = LogProbs._here(N, K, top)
     status = _status(check and K > 0, dev)
-    rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V), logits.data_ptr(), _at(tokens),
-                                    _at(out.logp), out.entropy.data_ptr(), out.lse.data_ptr(), _at(out.top_logp),
-                                    _at(out.top_ids), _at(status), _queue(dev))
-    _finish(rc, status)
+    rc = lib().frnnt_token_logprobs(LogprobDims(N, V, K, top, dt, ld, V, out.lse_rest.data_ptr()),
+                                    logits.data_ptr(), _at(tokens), _at(out.logp), out.entropy.data_ptr(),
+                                    out.lse.data_ptr(), _at(out.top_logp), _at(out.top_ids), _at(status), _queue(dev))
+    if rc or status is not None:
+        _finish(rc, status)
     return out
 
 
@@ -721,8 +733,7 @@ def token_logprobs_bwd(logits, tokens, fwd: LogProbs, dlogp=None, dentropy=None,
     each of dlogp [N, K], dentropy [N] and dtop [N, top] (fp32) may be None.
     ``out`` [N, V] may be ``logits`` itself (written in place)."""
     top = 0 if fwd.top_ids is None else fwd.top_ids.shape[-1]
-    dt, N, V, K = _check_logprobs(logits, tokens, top)
-    ld = _rows("logits", logits)
+    dt, N, V, K, ld = _check_logprobs(logits, tokens, top)
     dev = logits.device
     _check_result(fwd, N, K, top, dev)
     if dlogp is not None:
@@ -743,9 +754,10 @@ def token_logprobs_bwd(logits, tokens, fwd: LogProbs, dlogp=None, dentropy=None,
     else:
         ldd = _rows("out", out)
     status = _status(check, dev)
-    rc = lib().frnnt_token_logprobs_bwd(LogprobDims(N, V, K, top, dt, ld, ldd), logits.data_ptr(), _at(tokens),
-                                        fwd.lse.data_ptr(), fwd.entropy.data_ptr(), _at(fwd.top_ids), _at(dlogp),
-                                        _at(dentropy), _at(dtop), out.data_ptr(), _at(status), _queue(dev))
+    rc = lib().frnnt_token_logprobs_bwd(LogprobDims(N, V, K, top, dt, ld, ldd, fwd.lse_rest.data_ptr()),
+                                        logits.data_ptr(), _at(tokens), fwd.lse.data_ptr(), fwd.entropy.data_ptr(),
+                                        _at(fwd.top_ids), _at(dlogp), _at(dentropy), _at(dtop), out.data_ptr(),
+                                        _at(status), _queue(dev))
     _finish(rc, status)
     return out
 

@@ -95,8 +95,9 @@ def test_plain_fp32_is_within(V, shift, scale):
             w = np.concatenate([e * d, np.zeros(pad, f)]).reshape(-1, 8).cumsum(0, dtype=f)[-1].sum(dtype=f)
             ls = np.log(s)
             lse, entropy = f(m + ls), f(ls - f(0.6931471805599453) * (w / s))
+            rest = (m - (lse - (lse - m))) + (ls - (lse - m))
             logp = (row[tokens[n]] - m) - ls
-            q = np.maximum((row - lse) * f(1.4426950408889634), f(-160))
+            q = np.maximum(((row - lse) - rest) * f(1.4426950408889634), f(-160))
             grad = np.exp2(q) * (f(-dent[n] * f(0.6931471805599453)) * q - (dent[n] * entropy + dlogp[n].sum(dtype=f)))
         for t, c in zip(tokens[n], dlogp[n]):
             grad[t] += c
