@@ -121,6 +121,7 @@ StageScope::~StageScope() {
 using namespace frnnt;
 
 extern "C" FRNNT_API int frnnt_profile(int enable) {
+  std::lock_guard<std::mutex> guard(g_mu);
   g_timing = enable != 0;
   return FRNNT_OK;
 }
