@@ -205,9 +205,13 @@ struct Trial {
 // of every block sends it to every block's shared memory, where an mbarrier
 // counts the bytes of all CL maps.  Two buffers: a warp that sends round r + 2
 // has received round r + 1 from all, and each sent that after it had read round r.
-// A wait that runs out ends the block: it neither sends nor arrives again, so the
-// others' waits run out a round later at the latest, and it leaves when no map
-// can still come (see leave).
+// A wait that runs out ends the block after its round: it neither sends nor
+// arrives again, so the others' waits run out a round later at the latest, and it
+// leaves when no map can still come (see leave).  Beside waits that went on
+// regardless this costs nothing to 2 % (2 x 32749 x 1024 bf16: 94 -> 91 us, backward
+// 148; 3 x 10000 x 1024: 44.4 -> 45.7 and 68.0 -> 69.4; 2 x 16384 x 1023: 84 -> 85
+// and 138 -> 139).  With a vote of the lanes and a branch in the first warp's way the
+// backward passes took up to 163 and 147.
 template <int CL>
 struct Exchange {
   static constexpr uint32_t kBytes = 32 * sizeof(ulonglong2);   // of a map
@@ -222,8 +226,9 @@ struct Exchange {
       sm100::mbar_init(&full[1], 1);
       sm100::fence_barrier_init();
       gave_up = 0;
+#pragma unroll
+      for (int k = 0; k < CL; ++k) sent[k] = INT_MAX;   // (a thread each: 146 for 139 us, see above)
     }
-    if (threadIdx.x < CL) sent[threadIdx.x] = INT_MAX;
   }
   __device__ __forceinline__ void send(int r, int rank, int rounds, int lane, Map m, const Trial& trial) {
     if (lane == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * kBytes);
@@ -241,17 +246,15 @@ struct Exchange {
       ok = sm100::mbar_try_wait_cluster(&full[r & 1], (r >> 1) & 1, sm100::kSuspendNs);
     return ok;
   }
-  // The carry after this round; `in`: what enters block `rank`'s chunk.  When the
-  // wait runs out (for all lanes alike), gave_up is set and the carry means nothing.
+  // The carry after this round; `in`: what enters block `rank`'s chunk.  A lane
+  // whose wait runs out says so in gave_up, which all warps see after the next
+  // block barrier; its carry means nothing.
   __device__ __forceinline__ uint64_t receive(int r, int rank, int rounds, int lane, uint64_t carry, uint64_t& in,
                                               const Trial& trial, int32_t* status) {
     const bool ok = !trial.here(Trial::kQuit, r, rank, rounds) && wait(r, trial.tries);
-    if (!__all_sync(0xFFFFFFFFu, ok)) {
-      if (lane == 0) {
-        gave_up = r + 1;
-        if (status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
-      }
-      return carry;
+    if (!ok) {
+      gave_up = r + 1;
+      if (status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
     }
     for (int k = 0; k < CL; ++k) {
       if (k == rank) in = carry;
@@ -294,6 +297,7 @@ struct Exchange {
 template <>
 struct Exchange<1> {
   __device__ __forceinline__ void init() {}
+  static constexpr int gave_up = 0;
 };
 
 // Forward.  h_t = a_t h_{t-1} + b_t composes: over a run of steps h_out = A h_in
@@ -377,8 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL == 1) carry = in;
     }
     __syncthreads();
-    if constexpr (CL > 1)
-      if (ex.gave_up) break;
+    const bool stop = CL > 1 && ex.gave_up != 0;   // read early, used after the run
     uint64_t s = run[w][lane].y;
     if (VEC && whole && t0 + kSteps <= len) {
       char* base = reinterpret_cast<char*>(h + b * d.h_sb + c0 + (long long)(r * CL + rank) * kChunk * d.h_st);
@@ -405,6 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           store_pair<T, VEC>(out, t0 + i < len ? f2_open(s) : make_float2(0.f, 0.f), two);
       }
     }
+    if (stop) break;
   }
   // rows of whole rounds past the sequence
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
@@ -506,8 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL == 1) carry = in;
     }
     __syncthreads();
-    if constexpr (CL > 1)
-      if (ex.gave_up) break;
+    const bool stop = CL > 1 && ex.gave_up != 0;   // read early, used after the run
     v = run[w][lane].y;
     q = back[w][lane];
 #pragma unroll
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         }
       }
     }
+    if (stop) break;
   }
   for (int t = rounds * CL * kChunk + rank * nw + w; t < d.T; t += CL * nw)
     if (live) {
