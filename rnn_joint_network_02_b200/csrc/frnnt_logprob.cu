@@ -770,7 +770,8 @@ struct BwdParams {
   const int32_t *tokens, *top_ids;
   const float *lse, *entropy, *dlogp, *dentropy, *dtop;
   int32_t* status;
-  const float* lse_rest;   // or NULL: 0
+  const float* lse_rest;   // lse, with a factor of 0, where there is none
+  float rest_factor;       // else -log2 e
 };
 
 template <typename T>
@@ -798,8 +799,8 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[16 / sizeof(T)]
 // lowest value).  dz_j = 2^d_j 2^c (A + B c + B d_j) costs nothing an element.
 struct Slope {
   float l, A, B;
-  static __device__ __forceinline__ Slope of(float l, float rest, float A, float B) {
-    const float c = -kLog2e * rest, f = exp2_approx(c);
+  static __device__ __forceinline__ Slope of(float l, float c, float A, float B) {
+    const float f = exp2_approx(c);
     return Slope{l, f * fmaf(B, c, A), f * B};
   }
   __device__ __forceinline__ float at(float z) const {
@@ -835,9 +836,7 @@ struct Slope {
     }
   }
 };
-__device__ __forceinline__ float rest_of(const BwdParams& p, long long n) {
-  return p.lse_rest ? p.lse_rest[n] : 0.f;
-}
+__device__ __forceinline__ float rest_of(const BwdParams& p, long long n) { return p.rest_factor * p.lse_rest[n]; }
 // A lane's vectors, 32 apart, of a warp's share [base, end) of a row.  SKEW: rows
 // may start elsewhere in their 16 bytes than the gradient's.  Then vector v of 16-
 // bit elements lies in two aligned ones, v and v + 1 (both hold some of the row);
@@ -1010,7 +1009,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdPara
 #pragma unroll
   for (int e = 0; e < C; ++e) z[e] = g + G * e < p.V ? to_f32<T>(row[g + G * e]) : 0.f;
   const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
-  const float rest = rest_of(p, n);
+  const float c = rest_of(p, n);
   bool any = p.dentropy != nullptr;
   const int nk = p.dlogp ? p.K : 0, slots = nk + (p.dtop ? p.top : 0);
 #pragma unroll 2
@@ -1026,10 +1025,13 @@ __global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdPara
       atomicOr(p.status, FRNNT_STATUS_LABEL);
     }
   }
-  const Slope s = Slope::of(l, rest, -fmaf(de, h, sum), -de * kLn2);
+  const float A = -fmaf(de, h, sum), B = -de * kLn2;   // (few columns a lane: see Slope)
 #pragma unroll
-  for (int e = 0; e < C; ++e)   // a row without any term, or with nothing left by its mask, gets zeros
-    if (g + G * e < p.V) out[g + G * e] = from_f32<T>(!any || l == -INFINITY ? 0.f : s.at(z[e]) + total[e]);
+  for (int e = 0; e < C; ++e) {   // a row without any term, or with nothing left by its mask, gets zeros
+    const float d = at_least(fmaf(z[e] - l, kLog2e, c), kFloor);
+    if (g + G * e < p.V)
+      out[g + G * e] = from_f32<T>(!any || l == -INFINITY ? 0.f : fmaf(exp2_approx(d), fmaf(B, d, A), total[e]));
+  }
 }
 
 // Any row: `segments` warps share it (no reduction: each needs the row's scalars
@@ -1070,7 +1072,7 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
     }
   }
   const float l = p.lse[n], de = p.dentropy ? p.dentropy[n] : 0.f, h = p.dentropy ? p.entropy[n] : 0.f;
-  const float rest = rest_of(p, n);
+  const float c = rest_of(p, n);
   float sum = coef[0] + coef[1];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
@@ -1083,7 +1085,7 @@ __global__ void __launch_bounds__(kWarps * 32) logprob_bwd_kernel(BwdParams p, c
   }
   // a row without any term, or with nothing left by its mask, gets zeros
   const bool none = l == -INFINITY || (!p.dentropy && !__any_sync(kAll, id[0] >= 0 || id[1] >= 0));
-  const Slope g = Slope::of(l, rest, -fmaf(de, h, sum), -de * kLn2);
+  const Slope g = Slope::of(l, c, -fmaf(de, h, sum), -de * kLn2);
   auto patch = [&](int lo, int hi) {   // columns lo .. hi - 1 have been written by this warp
     __syncwarp();
 #pragma unroll
@@ -1294,7 +1296,8 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   {
     StageScope sc("token_logprobs_bwd", st);
     const BwdParams p{d->N, d->V, d->K,    d->top, 1,     0,        d->ld, d->ldd,
-                      tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,  status, d->lse_rest};
+                      tokens, top_ids, lse, entropy, dlogp, dentropy, dtop,  status,
+                      d->lse_rest ? d->lse_rest : lse, d->lse_rest ? -kLog2e : 0.f};
     if (d->dtype == FRNNT_BF16) launch_bwd(p, (const __nv_bfloat16*)logits, (__nv_bfloat16*)dlogits, st);
     else launch_bwd(p, (const float*)logits, (float*)dlogits, st);
   }
