@@ -52,8 +52,8 @@ FRNNT_API int frnnt_test_lose_gemm_loads(int n);
  * launches of frnnt_recurrence_fwd / _bwd whose sequences are shared by a
  * cluster of blocks, block 0 of every cluster withholds the message of one
  * round (quit = 0), so that every block's bounded wait in that round runs out;
- * or (quit = 1) sends it and gives up at once, so that the others' waits run
- * out in the next round, if there is one.  `round` counts from a sequence's
+ * or (quit = 1) takes part in the round and then gives up as if its wait had
+ * run out, so that the others' waits run out in the next round, if there is one.  `round` counts from a sequence's
  * first round, or, when negative, from its last (-1); `tries` replaces the
  * waits' limit (polls of 0.1 ms, 20000 at most).  Every block of the cluster
  * then stops, waits (with the same limit) for the messages that were sent to

@@ -191,13 +191,13 @@ __device__ __forceinline__ Map then(Map f, Map g) { return Map{f2_mul(g.A, f.A),
 __device__ __forceinline__ uint64_t apply(Map f, uint64_t v) { return f2_fma(f.A, v, f.R); }
 
 // A launch in which the exchange below fails on purpose (frnnt_test_lose_scan_maps): block 0 of every cluster, in one
-// round (counted from the last when negative), sends no map (kLose), or sends it and gives up without waiting (kQuit).
+// round (counted from the last when negative), sends no map (kLose), or behaves as if its wait had run out (kQuit).
 struct Trial {
   enum { kNone, kLose, kQuit };
   int kind = kNone, round = 0;
   uint32_t tries = sm100::kMaxTries;   // polls of a wait
-  __device__ __forceinline__ bool here(int what, int r, int rank, int rounds) const {
-    return kind == what && rank == 0 && r == (round < 0 ? rounds + round : round);
+  __device__ __forceinline__ int of(int rank, int rounds) const {   // the round in which this block is to fail
+    return kind == kNone || rank != 0 ? -1 : round < 0 ? rounds + round : round;
   }
 };
 
@@ -230,9 +230,9 @@ struct Exchange {
       for (int k = 0; k < CL; ++k) sent[k] = INT_MAX;   // (a thread each: 146 for 139 us, see above)
     }
   }
-  __device__ __forceinline__ void send(int r, int rank, int rounds, int lane, Map m, const Trial& trial) {
+  __device__ __forceinline__ void send(int r, int rank, int lane, Map m, int odd, const Trial& trial) {
     if (lane == 0) sm100::mbar_arrive_expect_tx(&full[r & 1], CL * kBytes);
-    if (trial.here(Trial::kLose, r, rank, rounds)) return;
+    if (r == odd && trial.kind == Trial::kLose) return;
 #pragma unroll
     for (int k = 0; k < CL; ++k)
       asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
@@ -249,9 +249,9 @@ struct Exchange {
   // The carry after this round; `in`: what enters block `rank`'s chunk.  A lane
   // whose wait runs out says so in gave_up, which all warps see after the next
   // block barrier; its carry means nothing.
-  __device__ __forceinline__ uint64_t receive(int r, int rank, int rounds, int lane, uint64_t carry, uint64_t& in,
+  __device__ __forceinline__ uint64_t receive(int r, int rank, int lane, uint64_t carry, uint64_t& in, int odd,
                                               const Trial& trial, int32_t* status) {
-    const bool ok = !trial.here(Trial::kQuit, r, rank, rounds) && wait(r, trial.tries);
+    const bool ok = wait(r, trial.tries) && !(r == odd && trial.kind == Trial::kQuit);
     if (!ok) {
       gave_up = r + 1;
       if (status) atomicOr(status, FRNNT_STATUS_TIMEOUT);
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   for (int r = 0; r < STAGES - 1; ++r) fetch(r);
   uint64_t carry = load_state<kApart<T, VEC>>(h0, b, d.D, c, live, two);
   if (CL > 1) cluster_wait();     // the other blocks run, their mbarriers are ready
+  [[maybe_unused]] const int odd = trial.of(rank, rounds);
   for (int r = 0; r < rounds; ++r) {
     const int t0 = (r * CL + rank) * kChunk + w * kSteps;
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -369,8 +370,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL > 1) {
         Map all = map_one();
         for (int k = 0; k < nw; ++k) all = then(all, Map{run[k][lane].x, run[k][lane].y});
-        ex.send(r, rank, rounds, lane, all, trial);
-        carry = ex.receive(r, rank, rounds, lane, carry, in, trial, status);
+        ex.send(r, rank, lane, all, odd, trial);
+        carry = ex.receive(r, rank, lane, carry, in, odd, trial, status);
       }
       if (t0 < len) store_state<kApart<T, VEC>>(saved, (long long)b * nc + t0 / kChunk, d.D, c, live, two, in);
       for (int k = 0; k < nw; ++k) {
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   for (int r = 0; r < STAGES - 1; ++r) fetch(r);
   uint64_t carry = load_state<kApart<T, VEC>>(dh_last, b, d.D, c, live, two);
   if (CL > 1) cluster_wait();
+  [[maybe_unused]] const int odd = trial.of(rank, rounds);
   for (int r = 0; r < rounds; ++r) {
     const int t0 = chunk_at(r) + w * kSteps;
     uint64_t v = f2_of(0.f, 0.f);   // (the first warp's)
@@ -494,14 +496,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if constexpr (CL > 1) {
         Map all = map_one();
         for (int k = nw - 1; k >= 0; --k) all = then(all, Map{run[k][lane].x, back[k][lane]});
-        ex.send(r, rank, rounds, lane, all, trial);
+        ex.send(r, rank, lane, all, odd, trial);
       }
       for (int k = 0; k < nw; ++k) {
         const ulonglong2 o = run[k][lane];
         run[k][lane].y = v;
         v = apply(Map{o.x, o.y}, v);
       }
-      if constexpr (CL > 1) carry = ex.receive(r, rank, rounds, lane, carry, in, trial, status);
+      if constexpr (CL > 1) carry = ex.receive(r, rank, lane, carry, in, odd, trial, status);
       for (int k = nw - 1; k >= 0; --k) {
         const uint64_t o = back[k][lane];
         back[k][lane] = in;
