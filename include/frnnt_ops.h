@@ -12,13 +12,15 @@
  * FRNNT_ERR_* codes returned before any launch.  Calls may come from several host threads at once and may be
  * captured into CUDA graphs.  Differences, because these calls take views of larger arrays and can be a few
  * microseconds long:
- *   - rows may be strided (strides in elements); pointers need the alignment of their element type only;
+ *   - rows may be strided (strides in elements); pointers need the alignment of their element type only.  Where a
+ *     row does not start or end on a 16-byte boundary, the whole aligned 16-byte unit around that end may be read (up
+ *     to 15 bytes before or behind the row, whose values do not matter); writes stay inside the rows;
  *   - no workspace is needed;
  *   - `status` may be NULL.  When given, invalid device-side values OR their FRNNT_STATUS_* bits into it: the
  *     call never clears it, the caller does.  After a bit was set the outputs of the rows concerned are
- *     unspecified; no access out of bounds happens either way.  FRNNT_STATUS_TIMEOUT: a bounded wait of the
- *     recurrence's blocks for each other gave up (after about 2 s; the call then ends within a few seconds, and
- *     later calls are not concerned).
+ *     unspecified; no access out of bounds happens either way (but for those units).  FRNNT_STATUS_TIMEOUT: a
+ *     bounded wait of the recurrence's blocks for each other gave up (after about 2 s; the call then ends within a
+ *     few seconds, and later calls are not concerned).
  * Outputs must not overlap inputs except where a call says so.
  */
 #ifndef FRNNT_OPS_H
@@ -76,9 +78,10 @@ FRNNT_API int frnnt_token_logprobs(const frnnt_logprob_dims* d, const void* logi
  * FRNNT_NO_TOKEN contributes nothing; a token or top id outside [0, V) otherwise sets FRNNT_STATUS_LABEL and
  * contributes nothing.  p_j comes from lse and, where given, lse_rest, as the forward call wrote them; without
  * lse_rest every p_j is off by a factor of exp(2^-24 |lse|) at most, and in a row of huge logits (all of them the
- * type's lowest value, say) p means nothing.  dlogits [N, ldd] has the type of the logits, rounded once; it may be the logits' own
- * memory (same address and ldd = ld).  A row of -inf only gets zeros, and so does a row without any term (no
- * given token, dtop and dentropy NULL) whatever it holds; elements of the rows past V are not written. */
+ * type's lowest value, say) p means nothing.  dlogits [N, ldd] has the type of the logits, rounded once; it may
+ * be the logits' own memory (same address and ldd = ld).  A row of -inf only gets zeros, and so does a row without
+ * any term (no given token, dtop and dentropy NULL) whatever it holds; elements of the rows past V are not
+ * written. */
 FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, const void* logits, const int32_t* tokens,
                                        const float* lse, const float* entropy, const int32_t* top_ids,
                                        const float* dlogp, const float* dentropy, const float* dtop, void* dlogits,
@@ -148,10 +151,10 @@ typedef struct {
 } frnnt_dropout_dims;
 
 /* y = x / (1 - p) where the element stays, 0 where it is dropped (also if x is NaN or infinite there).
- * Element e (row-major index r * C + c) takes 16 bits of the Philox4x32-10 block of key seed and 128-bit
- * counter offset + e / 8 ("Parallel Random Numbers: As Easy as 1, 2, 3"): half-word e % 8 of its four words, low
- * halves first; it stays where those bits are >= P = round(65536 p), and is scaled by 65536 / (65536 - P).  So
- * the mask depends on seed, offset and the element's index alone: not on type, strides or device, and the same
+ * Element e (row-major index r * C + c) takes 16 bits of the Philox4x32-10 block of key seed and counter
+ * (offset + e / 8) mod 2^64, the counter's upper 64 bits 0 ("Parallel Random Numbers: As Easy as 1, 2, 3"):
+ * half-word e % 8 of its four words, low halves first; it stays where those bits are >= P = round(65536 p), and is
+ * scaled by 65536 / (65536 - P).  So the mask depends on seed, offset and the element's index alone: not on type, strides or device, and the same
  * call on dy gives dx.  Arrays that follow each other in one stream of numbers take offsets at least
  * ceil(R C / 8) apart.
  *   rng  [2] uint64 device array or NULL: when given, rng[0] replaces d->seed and rng[1] is added to d->offset (a

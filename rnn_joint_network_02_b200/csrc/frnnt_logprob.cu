@@ -348,7 +348,9 @@ __device__ __forceinline__ void collect_short(const Row<T>& row, int lane, const
 // Rows that the bound does not thin out (many equal values, or fewer than `top`
 // elements above -inf): one warp goes through the row in order, with the list
 // of the best so far, which stops later columns of equal value.  Descending,
-// one a lane; `buffer`: 64 places.
+// one a lane; `buffer`: 64 places.  Latency of a load and a ballot every 32
+// columns, 0.27 us: 7 x 131071 bf16 with 5 columns left, or all equal, 1.1 ms (7 us
+// where a bound thins the rows out); 64 x 4096 fp32 22 to 25 us (4).
 template <typename T>
 __device__ __noinline__ uint64_t best_in_order(const T* p, int V, int top, uint64_t* buffer) {
   const int lane = threadIdx.x & 31;
@@ -451,11 +453,12 @@ struct Share {
 };
 
 // Rows of a few KB.  One pass over the row with a running maximum and sums in
-// fp32; bound by the pass over memory (2 bytes a 16-bit element), in practice
-// by what surrounds one exponential an element: 380 instructions a row of 1024,
-// of which 200 are the elements'.  32400 x 1024 bf16: 18.3 us (3.6 TB/s; with 10
+// fp32.  Bound by latency: 370 instructions a row of 1024 (200 are the elements')
+// fill 62 % of the issue slots, the exponentials 46 % of their unit and the loads 40 %
+// of DRAM, with 24 warps an SM (80 registers) and 15 dependent shuffles at the end
+// of a row.  32400 x 1024 bf16: 18.7 us (3.5 TB/s; with 10
 // rows for most warps instead of 9 or 10 for each: 20.3; a warp a row without a
-// next one on its way: 31), with the best 8: 36 us, 20: 45 us.
+// next one on its way: 31), with the best 8: 37 us, 20: 45 us.
 // A warp takes its share of rows, one after another, with the next one's vectors
 // on their way.  Lane i keeps row i's joined statistics, so that the logarithms,
 // divisions and stores of up to 32 rows are made at once, a lane a row; the
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // with C of its columns, G apart, element by element (any alignment; a warp's
 // rows lie next to each other, so its accesses cover whole sectors all the same).
 // Everything is in registers: bound by the instructions of each element.  60000
-// x 128 bf16: 10.4 us (1.9 TB/s), x 24: 3.3 us.  A candidate for the alternatives
+// x 128 bf16: 10.7 us (1.4 TB/s), x 24: 3.5 us.  A candidate for the alternatives
 // finds its place by counting the larger ones: of the whole row, or, with a warp
 // a row, of what reaches the bound.
 template <typename T, int G, int C, bool TOP>
@@ -902,7 +905,7 @@ struct Vecs {
 };
 
 // Bound by memory: a row is read and its gradient written.  32400 x 1024 bf16:
-// 22.7 us (5.8 TB/s; a warp a row with its scalars loaded row by row: 34 us).
+// 23.7 us (5.6 TB/s; a warp a row with its scalars loaded row by row: 34 us).
 // Rows of a few KB with few coefficients: a warp takes its share of rows, one
 // after another, with the next one's vectors on their way.  Lane i prepares row i's slope
 // (the loads of up to 32 rows' scalars at once) and, when all rows are
@@ -996,8 +999,9 @@ __global__ void __launch_bounds__(kWarps * 32, SKEW && sizeof(T) == 2 ? 2 : 3)
 // Short rows: G lanes a row, as in the forward pass.  Every lane goes through the
 // row's coefficients and adds up those of its own columns, so no column is
 // written twice and every element is read and written by one lane (dlogits may be
-// the logits' memory).  Bound by latency: five blocks an SM, 60000 x 128 bf16, two
-// tokens and the entropy: 16.0 us (four: 18.3, six: 16.7), x 24: 4.6.
+// the logits' memory).  Bound by latency and instructions (70 % of the issue slots,
+// loads awaited): five blocks an SM, 60000 x 128 bf16, two tokens and the entropy:
+// 16.1 us (of the form before: four 18.3, five 16.0, six 16.7), x 24: 4.8.
 template <typename T, int G, int C>
 __global__ void __launch_bounds__(kWarps * 32, 5) logprob_bwd_few_kernel(BwdParams p, const T* logits, T* dlogits) {
   const int lane = threadIdx.x & 31, g = lane % G;
@@ -1129,8 +1133,8 @@ bool take(Go go) {
   note_launch();
   return true;
 }
-// 60000 rows of 24 / 64 / 128 / 256 / 512 bf16 logits: 3.3 / 5.2 / 10.4 / 15.2 / 25.4 us here, 22 / 23 / 24 / 25 / 28
-// in logprob_warp_kernel (fp32 3.6 / 6.2 / 10.5 / 14.0 / 23.8 and 20 / 21 / 22 / 23 / 24)
+// 60000 rows of 24 / 64 / 128 / 256 / 512 bf16 logits: 3.5 / 5.5 / 10.6 / 15.3 / 25.7 us here, 22 / 23 / 24 / 25 / 28
+// in logprob_warp_kernel (fp32 3.7 / 6.3 / 10.7 / 14.0 / 24.4 and 20 / 21 / 22 / 23 / 24)
 template <typename Go>
 bool with_few_fwd(int V, Go go) {
   if (V <= 16) return take<2, 8>(go);
@@ -1140,7 +1144,7 @@ bool with_few_fwd(int V, Go go) {
   if (V <= 256) return take<16, 16>(go);
   return V <= 512 && take<32, 16>(go);
 }
-// with the best 8 alternatives, 24 / 64 / 128 / 256 bf16 logits: 11 / 28 / 32 / 40 us here, 58 / 70 / 60 / 59 there
+// with the best 8 alternatives, 24 / 64 / 128 / 256 bf16 logits: 12 / 29 / 33 / 40 us here, 58 / 70 / 60 / 59 there
 template <typename Go>
 bool with_few_top(int V, Go go) {
   if (V <= 16) return take<4, 4>(go);
@@ -1149,9 +1153,9 @@ bool with_few_top(int V, Go go) {
   if (V <= 128) return take<32, 4>(go);
   return V <= 256 && take<32, 8>(go);
 }
-// The gradient, whose every lane goes through all coefficients.  2 of them, 24 / 64 / 128 / 256 logits: 4.6 / 8.0 /
+// The gradient, whose every lane goes through all coefficients.  2 of them, 24 / 64 / 128 / 256 logits: 4.8 / 8.3 /
 // 16 / 33 us here (256 with 16 columns a lane), 21 / 21 / 23 / 24 in logprob_bwd_rows_kernel; 8 of them, 64 / 128: 14 /
-// 25 here, 38 / 41 in logprob_bwd_kernel; 24 of them: 29 / 55 and 48 / 49
+// 25 here, 38 / 41 in logprob_bwd_kernel; 24 of them: 29 / 55 and 48 / 47
 template <typename Go>
 bool with_few_bwd(int V, int slots, Go go) {
   if (V <= 16) return take<2, 8>(go);
@@ -1256,7 +1260,8 @@ extern "C" FRNNT_API int frnnt_token_logprobs(const frnnt_logprob_dims* d, const
     return FRNNT_ERR_NULL;
   if ((uintptr_t)logits % (d->dtype == FRNNT_BF16 ? 2 : 4)) return FRNNT_ERR_ALIGN;
   for (const void* p : {(const void*)tokens, (const void*)logp, (const void*)entropy, (const void*)lse,
-                        (const void*)top_logp, (const void*)top_ids, (const void*)status, (const void*)d->lse_rest})
+                        (const void*)top_logp, (const void*)top_ids, (const void*)status,
+                        (const void*)d->lse_rest})
     if ((uintptr_t)p % 4) return FRNNT_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
   cudaGetLastError();   // clear a stale error so it is not reported as ours
@@ -1289,7 +1294,8 @@ extern "C" FRNNT_API int frnnt_token_logprobs_bwd(const frnnt_logprob_dims* d, c
   const size_t es = d->dtype == FRNNT_BF16 ? 2 : 4;
   if ((uintptr_t)logits % es || (uintptr_t)dlogits % es) return FRNNT_ERR_ALIGN;
   for (const void* p : {(const void*)tokens, (const void*)lse, (const void*)entropy, (const void*)top_ids,
-                        (const void*)dlogp, (const void*)dentropy, (const void*)dtop, (const void*)status, (const void*)d->lse_rest})
+                        (const void*)dlogp, (const void*)dentropy, (const void*)dtop, (const void*)status,
+                        (const void*)d->lse_rest})
     if ((uintptr_t)p % 4) return FRNNT_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
   cudaGetLastError();   // clear a stale error so it is not reported as ours

@@ -310,10 +310,10 @@ struct Exchange<1> {
 // cluster take the chunks in turn.
 // Bound by memory (three elements moved a step and channel) where there are
 // tiles enough: 32 x 4096 x 1024 bf16 143 us (5.6 TB/s).  2 x 32749 x 1024 bf16,
-// clusters of 8: 94 us (4.3 TB/s), its 256 blocks not spread evenly over the
-// SMs and one exchange a round.  16 steps a thread, in registers, halve the
+// clusters of 8: 91 us (4.5 TB/s), its 256 blocks not spread evenly over the
+// SMs, and latency: one exchange and three block barriers a round.  16 steps a thread, in registers, halve the
 // work on maps against 8 (326 us, one element at a time); results put into
-// shared memory and written 16 bytes a lane were no faster (94 us).
+// shared memory and written 16 bytes a lane were no faster.
 template <typename T, bool VEC, int CL, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     scan_fwd_kernel(frnnt_recurrence_dims d, const T* __restrict__ x, const T* __restrict__ gate,
@@ -695,9 +695,11 @@ int resident() {
 
 // Blocks that share a sequence's chunks: as few as give the fewest rounds, of
 // those whose clusters run all at once.  bf16, forward and backward, with 8 at
-// most and powers of two only: 8 x 1500 x 513 23 us and 38, here (6) 17 and 27; 1 x
+// most and powers of two only: 8 x 1500 x 513 23 us and 38, here (6) 16 and 27; 1 x
 // 32749 x 64 61 and 91, here (16) 37 and 50.  Clusters that do not all fit: 3 x
-// 10000 x 1024 61 and 94 (48 of 6), here (5) 44 and 68.
+// 10000 x 1024 61 and 94 (48 of 6), here (5) 46 and 69.  Sizes 9 and 11 to 15 are
+// left out: each is eight kernels, and of the chunk and tile counts up to 256 and
+// 152, evenly spread over their logarithms, 8 % would take fewer rounds with them.
 template <typename Fit, typename Launch>
 int with_cluster(const frnnt_recurrence_dims& d, int tile, Fit fit, Launch launch) {
   const long long tiles = (long long)((d.D + tile - 1) / tile) * d.B;
@@ -736,7 +738,7 @@ int launch_scan(const frnnt_recurrence_dims& d, cudaStream_t st, A... args) {
   if (resident<T, ARRAYS, CL, kernel>() < 0) return FRNNT_ERR_CUDA;
   const int warps = d.T < kChunk ? (d.T + kSteps - 1) / kSteps : kWarps;
   const dim3 grid((d.D + TILE - 1) / TILE * CL, d.B);
-  // one round needs one chunk's memory, and a short one only its rows
+  // as many stages as there are rounds (whole ones, however short the last chunk)
   const int rounds = ((d.T + kChunk - 1) / kChunk + CL - 1) / CL;
   const int bytes =
       rounds >= stages_of(ARRAYS) ? kMostBytes<T, ARRAYS> : rounds * (int)sizeof(Stage<T>) * ARRAYS + kSlack;

@@ -310,7 +310,10 @@ class Dropout(NamedTuple):
     ``dropout`` (below) and is never stored: f's entries take the counters from
     ``offset`` on, g's those that follow.  A new call needs new numbers: another
     ``seed``, or ``offset`` moved on by ``counters(f, g)``; ``seed`` may be a
-    device tensor (captured graphs).  Data-parallel ranks need a seed each."""
+    device tensor (captured graphs).  Data-parallel ranks need a seed each.
+    f and g, and df and dg, are scaled in fp32 and rounded to their type once
+    more than in a call without dropout (the joint network takes and gives that
+    type)."""
     p: float
     seed: "int | torch.Tensor"
     offset: int = 0
