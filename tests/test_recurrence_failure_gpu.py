@@ -43,11 +43,9 @@ SHAPES = [(3, 300, 34, "plain", "bf16"), (1, 4200, 64, "plain", "bf16"), (30, 21
 
 
 @pytest.mark.parametrize("quit", [False, True])
-@pytest.mark.parametrize("round", [0, 1, 2, -1])
-@pytest.mark.parametrize("B,T,D,layout,dtype", SHAPES)
+@pytest.mark.parametrize("B,T,D,layout,dtype,round", [(*shape, r) for shape in SHAPES for r in (0, 1, 2, -1)
+                                                      if r <= 0 or shape[1] > 1000])
 def test_lost_map_times_out_and_context_survives(cuda_ok, lose_maps, B, T, D, layout, dtype, round, quit):
-    if round > 0 and T < 1000:
-        pytest.skip("one round only")
     x, gate, lengths, h0, dh, dl = make(B, T, D, dtype, layout, seed=51)
     r = frnnt.recurrence(x, gate, lengths=lengths, h0=h0)
     d = frnnt.recurrence_bwd(x, gate, r, dh, lengths=lengths, dh_last=dl)
