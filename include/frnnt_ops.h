@@ -107,7 +107,8 @@ typedef struct {
  *   saved   [B, ceil(T / FRNNT_SCAN_CHUNK), D] fp32 or NULL: the states before steps 0, 128, 256, ... that the
  *           backward call starts from (those at or past lengths[b] are not written)
  *   h0      [B, D] fp32 or NULL
- * The state is carried in fp32 and rounded only where it is written to h. */
+ * The state is carried in fp32 and rounded only where it is written to h; a and 1 - a are each good to a relative
+ * 2^-21 + |gate| 2^-24 (the rounding of an fp32 gate costs them as much). */
 FRNNT_API int frnnt_recurrence_fwd(const frnnt_recurrence_dims* d, const void* x, const void* gate,
                                    const int32_t* lengths, const float* h0, void* h, float* h_last, float* saved,
                                    int32_t* status, void* stream);
